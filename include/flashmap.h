@@ -34,6 +34,7 @@
 #ifndef FLASHMAP_H
 #define FLASHMAP_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -275,6 +276,131 @@ fm_status fm_verify_greedy_noalloc(const float *target_logits, const int32_t *dr
                                    int B, int N, int K, int V,
                                    int32_t *n_acc, int32_t *branch, int32_t *out_tokens,
                                    fm_stream stream);
+
+/* ---- The target's paged key/value cache.
+ * The target's rows that the verifier's logits come from (the last token and
+ * the drafted ones: P5 "Why drafting still costs time", one parallel pass of
+ * the target) attend over keys and values kept in pages.  The pages have no
+ * counterpart of these three operators; they are what a target that scores
+ * this library's drafts needs next to them: the new rows' head norms,
+ * rotation and append, the attention over the pages, and eviction.  They need
+ * no fm_ctx and allocate nothing.
+ *
+ * One layer's cache:
+ *   k, v         device [n_pages, n_kv_heads, page_size, head_dim] dtype
+ *   pos          device [n_pages, n_kv_heads, page_size] int32, the position
+ *                each cached row came from, or NULL: row r of a sequence has
+ *                position r (until an eviction reorders the rows)
+ *   weight       device [n_pages, n_kv_heads, page_size] fp32, the attention
+ *                weight each cached row got so far, or NULL
+ *   page_table   device [n_seqs, table_stride] int32; row r of sequence b
+ *                lives in page page_table[b][r / page_size].  Entries past a
+ *                sequence's rows are not read.  A row whose entry lies
+ *                outside [0, n_pages) does not exist: nothing is written to
+ *                it and no query sees it.
+ * page_size is 16, 32, 64 or 128; head_dim 64 or 128 (bf16), 32, 64 or 128
+ * (fp32); every array 16-byte aligned.  Pages may be shared by sequences that
+ * only read them.  Sequences of a call are rows 0 .. B-1 of the table,
+ * B <= FM_MAX_CALL_SEQS. */
+typedef struct {
+  int dtype, n_pages, page_size, n_kv_heads, head_dim, table_stride;
+  void *k, *v;
+  int32_t *pos;
+  float *weight;
+  const int32_t *page_table;
+} fm_paged_cache;
+
+/* New rows of a call, used by append and attention: sequence b owns rows
+ * cu_rows[b] .. cu_rows[b+1]-1 of the T given ones (cu_rows: device [B+1],
+ * ascending from 0), and kv_len[b] (device [B]) is its length in the cache
+ * with these rows, so its new row i is cache row kv_len[b] - n_b + i.  Rows at
+ * or past cu_rows[B] belong to no sequence and are left alone, in and out.
+ * q_pos (device [T], or NULL: the cache row) are the rows' positions. */
+
+/* Norms, rotation and append (n_heads a multiple of n_kv_heads):
+ *   q, k, v      device rows of [n_heads | n_kv_heads | n_kv_heads, head_dim]
+ *                dtype, `*_stride` elements apart (a multiple of 16 bytes), so
+ *                the three may be slices of one projection's output
+ *   q_gain, k_gain  device [head_dim] dtype: per head x / sqrt(mean(x^2) +
+ *                eps) * gain; NULL leaves the heads as they are
+ *   inv_freq     device fp64 [rot_dim / 2]: pair i of a head's first rot_dim
+ *                values turns by the angle position * inv_freq[i] (reduced in
+ *                fp64, so far positions keep their angles); NULL with rot_dim
+ *                0: no rotation.  rot_dim: a multiple of 16, at most head_dim
+ *   interleaved  0: pair i is values (i, i + rot_dim/2); 1: (2i, 2i + 1)
+ *   q_out        device [T] rows of [n_heads, head_dim], q_out_stride apart;
+ *                may be q itself (same stride)
+ * The rows' keys (after norm and rotation) and values go to their cache rows;
+ * with cache->pos their positions, with cache->weight zeros.  Sums, norms and
+ * angles are fp32 (angles reduced in fp64), each output rounded once. */
+typedef struct {
+  int T, B, n_heads;
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const void *q_gain, *k_gain;
+  float eps;
+  const double *inv_freq;
+  int rot_dim, interleaved;
+  const int32_t *cu_rows, *kv_len, *q_pos;
+  void *q_out;
+  int64_t q_out_stride;
+} fm_append_args;
+fm_status fm_cache_append(const fm_paged_cache *cache, const fm_append_args *a, fm_stream stream);
+
+/* Attention of the new rows over their sequences' cached rows (their own
+ * among them: append first).  Query head h reads key/value head
+ * h / (n_heads / n_kv_heads).  With p the positions, a query sees row r iff
+ * r < kv_len, p_r <= p_q, and (window > 0) p_q - p_r < window or p_r < sinks:
+ * a sliding window whose first `sinks` tokens stay visible.
+ *   q, out       device rows of [n_heads, head_dim] dtype, `*_stride` apart
+ *   max_rows     no sequence has more new rows (later ones are not computed)
+ *   max_kv       no sequence is longer (a longer one is cut to it)
+ *   scale        of the scores, > 0 (1/sqrt(head_dim) as a rule)
+ *   accumulate   != 0: cache->weight[row] += the probabilities the row gets,
+ *                summed over the new rows and the query heads of its head
+ *   lse          device [T, n_heads] fp32 log-sum-exp of the scores, or NULL
+ * With cache->pos q_pos must be given.  A query that sees nothing gets zeros
+ * and lse -inf.  Rows at or past kv_len and rows that no query of the call
+ * sees may hold anything, NaN included; a non-finite value in a row that some
+ * query sees can reach the sequence's other queries.  Running maxima, sums
+ * and outputs are fp32; bf16 probabilities enter the value product rounded
+ * to bf16.  Results do not depend on scheduling.
+ * ws: device, 256-byte aligned, at least what fm_cache_attention_workspace
+ * says for the same sizes on the current device; its contents need no set-up
+ * and mean nothing afterwards.  Calls that may overlap on the device (two
+ * streams, two graphs) need a workspace each. */
+typedef struct {
+  int T, B, n_heads, max_rows, max_kv;
+  const void *q;
+  int64_t q_stride;
+  const int32_t *cu_rows, *kv_len, *q_pos;
+  float scale;
+  int window, sinks, accumulate;
+  void *out;
+  int64_t out_stride;
+  float *lse;
+} fm_attention_args;
+fm_status fm_cache_attention_workspace(const fm_paged_cache *cache, const fm_attention_args *a,
+                                       size_t *bytes);
+fm_status fm_cache_attention(const fm_paged_cache *cache, const fm_attention_args *a, void *ws,
+                             size_t ws_bytes, fm_stream stream);
+
+/* Eviction by accumulated weight.  Every (sequence, key/value head) with more
+ * than `budget` rows keeps budget of them: first the rows whose position is
+ * below `sinks` or at least next_pos - recent, then those with the largest
+ * weight (NaN and negative weights count as 0), ties to the lowest cache row.
+ * The kept rows from cache row budget on move, in ascending order, into the
+ * evicted rows' places below it, keys, values, positions and weights; the
+ * other rows stay where they are.
+ *   kv_len, next_pos  device [B]: cached rows; the next token's position
+ *   new_len           device [B] out: min(kv_len, budget); not kv_len itself
+ * Needs cache->pos and cache->weight, pages that no other sequence of the
+ * call holds, sinks + recent <= budget and max_kv (no sequence is longer)
+ * <= FM_MAX_EVICT_ROWS (else FM_ERR_UNSUPPORTED).  Exact. */
+#define FM_MAX_EVICT_ROWS 262144
+fm_status fm_cache_evict(const fm_paged_cache *cache, const int32_t *kv_len,
+                         const int32_t *next_pos, int B, int max_kv, int budget, int sinks,
+                         int recent, int32_t *new_len, fm_stream stream);
 
 /* Reads and clears the context's device error word: FM_OK, or
  * FM_ERR_TIMEOUT when a bounded wait inside a kernel gave up (about two

@@ -21,6 +21,8 @@ Modules:
   tree).  Used at every size.
 * ``loops``     the same draft written with plain Python loops, for tiny
   shapes only; an independent second formulation.
+* ``cache``     the target-side cache operators: head norms and rotation, attention
+  under a window with sinks, eviction by weight.
 * ``toy_flow``  the exact flow of a two-mode data distribution ("new york" /
   "san diego"), used to check the flow-map update and shared-noise drafting.
 

@@ -21,12 +21,14 @@ FM_OK, FM_ERR_ARG, FM_ERR_CUDA, FM_ERR_OOM, FM_ERR_TIMEOUT, FM_ERR_UNSUPPORTED =
 FM_F32, FM_BF16 = 0, 1
 FM_MAX_CALL_SEQS = 256
 FM_MAX_STEPS = 8
+FM_MAX_EVICT_ROWS = 262144
 
 EXPORTS = (
     "fm_load_weights", "fm_free", "fm_last_error", "fm_project_context",
     "fm_draft", "fm_verify_greedy", "fm_verify_sample", "fm_profile", "fm_profile_read", "fm_device_status",
     "fm_verify_greedy_noalloc", "fm_draft_factorised", "fm_build_tree", "fm_tree_attention",
     "fm_verify_greedy_tree", "fm_verify_sample_tree", "fm_selftest_exp",
+    "fm_cache_append", "fm_cache_attention_workspace", "fm_cache_attention", "fm_cache_evict",
 )
 FM_PROF = {"embed": 0, "dit_gemm": 1, "attn": 2, "norm": 3, "lm_head": 4, "context": 5,
            "verify": 6, "other": 7}
@@ -53,6 +55,30 @@ class fm_weights(ctypes.Structure):
     _fields_ = [("E", _vp), ("W_lm", _vp), ("W_fc", _vp), ("W_ts1", _vp), ("W_ts2", _vp),
                 ("W_tt1", _vp), ("W_tt2", _vp), ("W_ada_f", _vp), ("W_qkv", _pvp),
                 ("W_o", _pvp), ("W_up", _pvp), ("W_down", _pvp), ("W_ada", _pvp)]
+
+
+_i, _i64 = ctypes.c_int, ctypes.c_int64
+
+
+class fm_paged_cache(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("n_pages", _i), ("page_size", _i), ("n_kv_heads", _i),
+                ("head_dim", _i), ("table_stride", _i), ("k", _vp), ("v", _vp), ("pos", _vp),
+                ("weight", _vp), ("page_table", _vp)]
+
+
+class fm_append_args(ctypes.Structure):
+    _fields_ = [("T", _i), ("B", _i), ("n_heads", _i), ("q", _vp), ("k", _vp), ("v", _vp),
+                ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64), ("q_gain", _vp),
+                ("k_gain", _vp), ("eps", ctypes.c_float), ("inv_freq", _vp), ("rot_dim", _i),
+                ("interleaved", _i), ("cu_rows", _vp), ("kv_len", _vp), ("q_pos", _vp),
+                ("q_out", _vp), ("q_out_stride", _i64)]
+
+
+class fm_attention_args(ctypes.Structure):
+    _fields_ = [("T", _i), ("B", _i), ("n_heads", _i), ("max_rows", _i), ("max_kv", _i),
+                ("q", _vp), ("q_stride", _i64), ("cu_rows", _vp), ("kv_len", _vp), ("q_pos", _vp),
+                ("scale", ctypes.c_float), ("window", _i), ("sinks", _i), ("accumulate", _i),
+                ("out", _vp), ("out_stride", _i64), ("lse", _vp)]
 
 
 _lib = None
@@ -102,6 +128,16 @@ def load_library(path: str = LIB_PATH):
     lib.fm_device_status.argtypes = [p, st]
     lib.fm_selftest_exp.restype = i
     lib.fm_selftest_exp.argtypes = [p, p, p, i, st]
+    cache = ctypes.POINTER(fm_paged_cache)
+    lib.fm_cache_append.restype = i
+    lib.fm_cache_append.argtypes = [cache, ctypes.POINTER(fm_append_args), st]
+    attn = ctypes.POINTER(fm_attention_args)
+    lib.fm_cache_attention_workspace.restype = i
+    lib.fm_cache_attention_workspace.argtypes = [cache, attn, ctypes.POINTER(ctypes.c_size_t)]
+    lib.fm_cache_attention.restype = i
+    lib.fm_cache_attention.argtypes = [cache, attn, p, ctypes.c_size_t, st]
+    lib.fm_cache_evict.restype = i
+    lib.fm_cache_evict.argtypes = [cache, p, p, i, i, i, i, i, p, st]
     lib.fm_profile.restype = i
     lib.fm_profile.argtypes = [p, i]
     lib.fm_profile_read.restype = i
@@ -274,3 +310,31 @@ def fm_verify_greedy_noalloc(target_logits, draft, B, N, K, V, n_acc, branch, ou
     _check(load_library().fm_verify_greedy_noalloc(_ptr(target_logits), _ptr(draft), B, N, K, V,
                                                    _ptr(n_acc), _ptr(branch), _ptr(out_tokens),
                                                    _stream(stream)))
+
+
+def fm_cache_append(cache: fm_paged_cache, args: fm_append_args, stream=None) -> None:
+    """Head norms, rotation and append of new rows (the structures hold device addresses)."""
+    _check(load_library().fm_cache_append(ctypes.byref(cache), ctypes.byref(args), _stream(stream)))
+
+
+def fm_cache_attention_workspace(cache: fm_paged_cache, args: fm_attention_args) -> int:
+    """Bytes of workspace fm_cache_attention needs on the current device."""
+    n = ctypes.c_size_t()
+    _check(load_library().fm_cache_attention_workspace(ctypes.byref(cache), ctypes.byref(args),
+                                                       ctypes.byref(n)))
+    return n.value
+
+
+def fm_cache_attention(cache: fm_paged_cache, args: fm_attention_args, ws, ws_bytes: int,
+                       stream=None) -> None:
+    """Attention of new rows over the paged cache."""
+    _check(load_library().fm_cache_attention(ctypes.byref(cache), ctypes.byref(args), _ptr(ws),
+                                             ws_bytes, _stream(stream)))
+
+
+def fm_cache_evict(cache: fm_paged_cache, kv_len, next_pos, B, max_kv, budget, sinks, recent,
+                   new_len, stream=None) -> None:
+    """Eviction by accumulated attention weight, in place."""
+    _check(load_library().fm_cache_evict(ctypes.byref(cache), _ptr(kv_len), _ptr(next_pos), B,
+                                         max_kv, budget, sinks, recent, _ptr(new_len),
+                                         _stream(stream)))

@@ -6,13 +6,15 @@ The library lands next to this file, so it travels with the source tree.
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libflashmap_b200.so")
-SRC = os.path.join(HERE, "csrc", "fm_api.cu")
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("fm_api.cu", "fm_cache_api.cu")]
+OBJ_DIR = os.path.join(HERE, "_build")
 
 
 def nvcc() -> str:
@@ -22,14 +24,18 @@ def nvcc() -> str:
     return "nvcc"
 
 
-def command(out: str = LIB, extra=()) -> list:
+def compile_command(src: str, obj: str, extra=()) -> list:
     return [
-        nvcc(), "-O3", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+        nvcc(), "-O3", "-std=c++17", "-c", "-Xcompiler", "-fPIC",
         "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
         "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc"),
         "--expt-relaxed-constexpr", "--extended-lambda",
-        *extra, SRC, "-o", out,
+        *extra, src, "-o", obj,
     ]
+
+
+def link_command(objs, out: str = LIB) -> list:
+    return [nvcc(), "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs, "-o", out]
 
 
 def sources() -> list:
@@ -46,20 +52,49 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in sources())
 
 
+def _newest(src: str, seen=None) -> float:
+    """Latest change of a source and of the headers it includes."""
+    seen = set() if seen is None else seen
+    seen.add(src)
+    t = os.path.getmtime(src)
+    for name in re.findall(r'#include "([^"]+)"', open(src, encoding="utf-8").read()):
+        for d in (os.path.dirname(src), os.path.join(ROOT, "include")):
+            f = os.path.join(d, name)
+            if os.path.exists(f) and f not in seen:
+                t = max(t, _newest(f, seen))
+    return t
+
+
+def _run(cmds, verbose: bool) -> None:
+    """Run the commands side by side; raise if one fails."""
+    if verbose:
+        for c in cmds:
+            print(" ".join(c), flush=True)
+    procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+             for c in cmds]
+    outs = [p.communicate()[0] for p in procs]
+    bad = any(p.returncode != 0 for p in procs)
+    if verbose or bad:
+        sys.stderr.write("".join(outs))
+    if bad:
+        raise RuntimeError("nvcc failed building libflashmap_b200.so")
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    """Compile every source (side by side) and link the library.  Objects
+    newer than their source and its headers are kept unless `force`."""
     if not force and up_to_date():
         return LIB
-    cmd = command(extra=extra)
-    if verbose:
-        print(" ".join(cmd), flush=True)
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    objs, cmds = [], []
+    for src in SRCS:
+        obj = os.path.join(OBJ_DIR, os.path.basename(src) + ".o")
+        objs.append(obj)
+        if force or not os.path.exists(obj) or os.path.getmtime(obj) < _newest(src):
+            cmds.append(compile_command(src, obj, extra))
+    _run(cmds, verbose)
     tmp = LIB + ".tmp"
-    cmd[cmd.index(LIB)] = tmp
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("nvcc failed building libflashmap_b200.so")
-    if verbose and (res.stdout or res.stderr):
-        sys.stderr.write(res.stdout + res.stderr)
+    _run([link_command(objs, tmp)], verbose)
     os.replace(tmp, LIB)
     return LIB
 

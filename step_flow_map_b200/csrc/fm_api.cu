@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "flashmap.h"
+#include "fm_host.cuh"
 #include "fm_simt.cuh"
 #include "fm_misc.cuh"
 #include "fm_verify.cuh"
@@ -22,27 +23,13 @@ using fm::bf16;
 // ------------------------------------------------------------------ errors
 static thread_local char g_err[1024] = "no error";
 
-static fm_status set_err(fm_status st, const char* fmt, ...) {
+fm_status set_err(fm_status st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_err, sizeof(g_err), fmt, ap);
   va_end(ap);
   return st;
 }
-
-#define FM_CUDA(call)                                                               \
-  do {                                                                              \
-    cudaError_t e_ = (call);                                                        \
-    if (e_ != cudaSuccess)                                                          \
-      return set_err(FM_ERR_CUDA, "%s failed: %s (%s:%d)", #call,                   \
-                     cudaGetErrorString(e_), __FILE__, __LINE__);                   \
-  } while (0)
-#define FM_LAUNCHED() FM_CUDA(cudaGetLastError())
-#define FM_TRY(expr)                  \
-  do {                                \
-    fm_status s_ = (expr);            \
-    if (s_ != FM_OK) return s_;       \
-  } while (0)
 
 extern "C" const char* fm_last_error(void) { return g_err; }
 

@@ -1,0 +1,344 @@
+// C ABI of the target's paged key/value cache: argument checks, variant
+// choice and launches of append, attention and eviction.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "flashmap.h"
+#include "fm_host.cuh"
+#include "fm_cache.cuh"
+#include "fm_cache_attn.cuh"
+
+using fm::bf16;
+
+namespace {
+
+constexpr int64_t MAX_ROWS = 1 << 24;      // new rows of a call, rows of a sequence
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+fm_status check_cache(const fm_paged_cache* c) {
+  if (!c || !c->k || !c->v || !c->page_table) return set_err(FM_ERR_ARG, "NULL argument");
+  if (c->dtype != FM_F32 && c->dtype != FM_BF16)
+    return set_err(FM_ERR_ARG, "unknown dtype %d", c->dtype);
+  if (c->n_pages < 1 || c->n_kv_heads < 1 || c->table_stride < 1)
+    return set_err(FM_ERR_ARG, "sizes must be positive");
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return set_err(FM_ERR_UNSUPPORTED, "page_size %d is not 16, 32, 64 or 128", c->page_size);
+  if (c->head_dim != 64 && c->head_dim != 128 && !(c->head_dim == 32 && c->dtype == FM_F32))
+    return set_err(FM_ERR_UNSUPPORTED, "head_dim %d is not 64 or 128 (or 32 in fp32)", c->head_dim);
+  if (c->n_kv_heads > 1024)
+    return set_err(FM_ERR_UNSUPPORTED, "n_kv_heads %d exceeds 1024", c->n_kv_heads);
+  // rows of the whole cache and of one table row are 31-bit numbers
+  if ((int64_t)c->n_pages * c->n_kv_heads > (int64_t)0x7fffffff / c->page_size ||
+      c->table_stride > MAX_ROWS / c->page_size)
+    return set_err(FM_ERR_UNSUPPORTED, "cache too large: pages x heads x page_size must stay below "
+                   "2^31, table_stride x page_size at most 2^24");
+  if (!aligned16(c->k) || !aligned16(c->v) || ((uintptr_t)c->pos & 3) || ((uintptr_t)c->weight & 3) ||
+      ((uintptr_t)c->page_table & 3))
+    return set_err(FM_ERR_ARG, "k and v must be 16-byte aligned, pos, weight and page_table 4-byte");
+  return FM_OK;
+}
+
+fm::CacheView view(const fm_paged_cache* c) {
+  fm::CacheView v;
+  v.n_pages = c->n_pages;
+  v.ps_log2 = __builtin_ctz((unsigned)c->page_size);
+  v.n_kv = c->n_kv_heads;
+  v.table_stride = c->table_stride;
+  v.k = c->k;
+  v.v = c->v;
+  v.pos = c->pos;
+  v.weight = c->weight;
+  v.table = c->page_table;
+  return v;
+}
+
+int esize(const fm_paged_cache* c) { return c->dtype == FM_F32 ? 4 : 2; }
+
+fm_status check_rows(const fm_paged_cache* c, int T, int B, int n_heads) {
+  if (T < 0 || B < 1 || n_heads < 1) return set_err(FM_ERR_ARG, "sizes must be positive");
+  if (B > FM_MAX_CALL_SEQS)
+    return set_err(FM_ERR_UNSUPPORTED, "B=%d exceeds %d sequences", B, FM_MAX_CALL_SEQS);
+  if (T > MAX_ROWS) return set_err(FM_ERR_UNSUPPORTED, "T=%d exceeds 2^24 rows", T);
+  if (n_heads > 4096) return set_err(FM_ERR_UNSUPPORTED, "n_heads %d exceeds 4096", n_heads);
+  if (n_heads % c->n_kv_heads)
+    return set_err(FM_ERR_ARG, "n_heads %d is not a multiple of n_kv_heads %d", n_heads,
+                   c->n_kv_heads);
+  return FM_OK;
+}
+
+// A row stride holds the row and keeps every row 16-byte aligned.
+fm_status check_stride(const fm_paged_cache* c, const char* name, const void* p, int64_t stride,
+                       int heads, int T) {
+  if (!p) return set_err(FM_ERR_ARG, "NULL %s", name);
+  if (!aligned16(p) || (stride * esize(c)) % 16)
+    return set_err(FM_ERR_ARG, "%s rows must be 16-byte aligned", name);
+  if ((T > 1 && stride < (int64_t)heads * c->head_dim) || stride < 0 || stride > ((int64_t)1 << 32))
+    return set_err(FM_ERR_ARG, "%s row stride %lld is too short for %d heads or out of range", name,
+                   (long long)stride, heads);
+  return FM_OK;
+}
+
+// SM count of the current device, asked once per device.
+fm_status device_sms(int* sms) {
+  static std::mutex mu;
+  static int known[64];
+  int dev = 0;
+  FM_CUDA(cudaGetDevice(&dev));
+  std::lock_guard<std::mutex> lock(mu);
+  int& k = known[dev & 63];
+  if (!k) FM_CUDA(cudaDeviceGetAttribute(&k, cudaDevAttrMultiProcessorCount, dev));
+  *sms = k;
+  return FM_OK;
+}
+
+#define FM_LAUNCH_OK(what, expr)                                                          \
+  do {                                                                                    \
+    cudaError_t e_ = (expr);                                                              \
+    if (e_ != cudaSuccess)                                                                \
+      return set_err(FM_ERR_CUDA, what " launch failed: %s", cudaGetErrorString(e_));     \
+  } while (0)
+
+}  // namespace
+
+// ------------------------------------------------------------------ append
+namespace {
+template <typename T, int DH>
+fm_status launch_append(const fm::AppendArgs& a, cudaStream_t st) {
+  FM_LAUNCH_OK("cache append",
+               fm::launch_pdl(fm::k_cache_append<T, DH>, dim3((unsigned)((a.T + a.tok - 1) / a.tok)),
+                              dim3(fm::CA_THREADS), 0, st, a));
+  return FM_OK;
+}
+}  // namespace
+
+extern "C" fm_status fm_cache_append(const fm_paged_cache* c, const fm_append_args* a,
+                                     fm_stream stream) {
+  FM_TRY(check_cache(c));
+  if (!a) return set_err(FM_ERR_ARG, "NULL argument");
+  FM_TRY(check_rows(c, a->T, a->B, a->n_heads));
+  if (!a->cu_rows || !a->kv_len) return set_err(FM_ERR_ARG, "NULL argument");
+  if (a->rot_dim < 0 || a->rot_dim > c->head_dim || a->rot_dim % 16)
+    return set_err(FM_ERR_ARG, "rot_dim %d is not a multiple of 16 up to head_dim %d", a->rot_dim,
+                   c->head_dim);
+  if (a->rot_dim > 0 && !a->inv_freq) return set_err(FM_ERR_ARG, "NULL inv_freq");
+  if ((uintptr_t)a->inv_freq & 7) return set_err(FM_ERR_ARG, "inv_freq must be 8-byte aligned");
+  if (!(a->eps >= 0.f) || a->eps > 1e30f) return set_err(FM_ERR_ARG, "eps must be finite and >= 0");
+  if (!aligned16(a->q_gain) || !aligned16(a->k_gain))
+    return set_err(FM_ERR_ARG, "gains must be 16-byte aligned");
+  if (c->pos && !a->q_pos)
+    return set_err(FM_ERR_ARG, "a cache with positions needs q_pos");
+  if (a->T == 0) return FM_OK;
+  FM_TRY(check_stride(c, "q", a->q, a->q_stride, a->n_heads, a->T));
+  FM_TRY(check_stride(c, "k", a->k, a->k_stride, c->n_kv_heads, a->T));
+  FM_TRY(check_stride(c, "v", a->v, a->v_stride, c->n_kv_heads, a->T));
+  FM_TRY(check_stride(c, "q_out", a->q_out, a->q_out_stride, a->n_heads, a->T));
+  fm::AppendArgs k;
+  k.c = view(c);
+  k.T = a->T;
+  k.B = a->B;
+  k.n_heads = a->n_heads;
+  k.q = a->q;
+  k.k = a->k;
+  k.v = a->v;
+  k.qs = a->q_stride;
+  k.ks = a->k_stride;
+  k.vs = a->v_stride;
+  k.os = a->q_out_stride;
+  k.qg = a->q_gain;
+  k.kg = a->k_gain;
+  k.eps = a->eps;
+  k.inv_freq = a->inv_freq;
+  k.rot = a->rot_dim;
+  k.interleaved = a->interleaved != 0;
+  k.cu = a->cu_rows;
+  k.kv_len = a->kv_len;
+  k.q_pos = a->q_pos;
+  k.q_out = a->q_out;
+  // rows per CTA: as many as its threads hold with CA_UNROLL loads each
+  const int per_row = (a->n_heads + 2 * c->n_kv_heads) * (c->head_dim * esize(c) / 16);
+  k.tok = std::max(1, std::min(fm::CA_MAX_TOK, fm::CA_THREADS * fm::CA_UNROLL / per_row));
+  cudaStream_t st = (cudaStream_t)stream;
+  if (c->dtype == FM_BF16)
+    return c->head_dim == 128 ? launch_append<bf16, 128>(k, st) : launch_append<bf16, 64>(k, st);
+  if (c->head_dim == 128) return launch_append<float, 128>(k, st);
+  return c->head_dim == 64 ? launch_append<float, 64>(k, st) : launch_append<float, 32>(k, st);
+}
+
+// ------------------------------------------------------------------ attention
+namespace {
+
+// What a call runs and where its workspace parts lie.
+struct AttnPlan {
+  int qt = 0, grid = 0;
+  int64_t tiles = 0;
+  size_t o_first = 0, o_tile = 0, o_lse = 0, o_ml = 0, o_part = 0, total = 0;
+};
+
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+fm_status check_attention(const fm_paged_cache* c, const fm_attention_args* a) {
+  FM_TRY(check_cache(c));
+  if (!a) return set_err(FM_ERR_ARG, "NULL argument");
+  FM_TRY(check_rows(c, a->T, a->B, a->n_heads));
+  if (a->max_rows < 1 || a->max_kv < 1) return set_err(FM_ERR_ARG, "sizes must be positive");
+  if (a->max_kv > MAX_ROWS) return set_err(FM_ERR_UNSUPPORTED, "max_kv %d exceeds 2^24", a->max_kv);
+  if (a->window < 0 || a->sinks < 0)
+    return set_err(FM_ERR_ARG, "window and sinks must not be negative");
+  if (a->accumulate && !c->weight) return set_err(FM_ERR_ARG, "accumulate needs cache->weight");
+  return FM_OK;
+}
+
+fm_status plan_attention(const fm_paged_cache* c, const fm_attention_args* a, AttnPlan* p) {
+  int sms = 0;
+  FM_TRY(device_sms(&sms));
+  const int64_t G = a->n_heads / c->n_kv_heads;
+  p->qt = a->max_rows * G <= 16 ? 16 : 64;
+  p->grid = 2 * sms;
+  p->tiles = ((int64_t)a->T * G) / p->qt + a->B;
+  size_t at = 256;
+  p->o_first = at;
+  at = up256(at + (size_t)(p->tiles + 1) * sizeof(long long));
+  p->o_tile = at;
+  at = up256(at + (size_t)p->tiles * 2 * sizeof(int4));
+  p->o_lse = at;
+  if (a->accumulate) at = up256(at + (size_t)a->T * a->n_heads * sizeof(float));
+  p->o_ml = at;
+  at = up256(at + (size_t)p->grid * 2 * p->qt * sizeof(float2));
+  p->o_part = at;
+  at = up256(at + (size_t)p->grid * 2 * p->qt * c->head_dim * sizeof(float));
+  p->total = at;
+  return FM_OK;
+}
+
+template <typename T, int DH, int QT>
+fm_status launch_simt(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_t st) {
+  using C = fm::CsCfg<DH, QT>;
+  FM_CUDA(fm::set_smem_once(fm::k_cache_attn_simt<T, DH, QT>, C::SMEM));
+  FM_LAUNCH_OK("cache attention plan",
+               fm::launch_pdl(fm::k_cache_plan<QT, fm::CS_KB>, dim3(1), dim3(fm::CP_THREADS), 0, st, k));
+  FM_LAUNCH_OK("cache attention", fm::launch_pdl(fm::k_cache_attn_simt<T, DH, QT>, dim3(p.grid),
+                                                 dim3(fm::CS_THREADS), C::SMEM, st, k));
+  FM_LAUNCH_OK("cache attention join",
+               fm::launch_pdl(fm::k_cache_join<T, DH, QT>, dim3(p.grid - 1, QT / 4),
+                              dim3(fm::CJ_THREADS), 0, st, k, p.grid));
+  return FM_OK;
+}
+
+template <typename T, int DH>
+fm_status run_attention(const fm::CacheAttnArgs& k, const AttnPlan& p, int accumulate,
+                        cudaStream_t st) {
+  if (p.qt == 16) FM_TRY((launch_simt<T, DH, 16>(k, p, st)));
+  else FM_TRY((launch_simt<T, DH, 64>(k, p, st)));
+  if (accumulate) {
+    const int per = fm::CW_THREADS / 32;
+    const int gx = std::max(1, std::min((k.max_kv + per - 1) / per, 64));
+    FM_LAUNCH_OK("cache weights",
+                 fm::launch_pdl(fm::k_cache_weights<T, DH>, dim3(gx, k.c.n_kv, k.B),
+                                dim3(fm::CW_THREADS), 0, st, k));
+  }
+  return FM_OK;
+}
+
+}  // namespace
+
+extern "C" fm_status fm_cache_attention_workspace(const fm_paged_cache* c,
+                                                  const fm_attention_args* a, size_t* bytes) {
+  if (!bytes) return set_err(FM_ERR_ARG, "NULL argument");
+  FM_TRY(check_attention(c, a));
+  AttnPlan p;
+  FM_TRY(plan_attention(c, a, &p));
+  *bytes = p.total;
+  return FM_OK;
+}
+
+extern "C" fm_status fm_cache_attention(const fm_paged_cache* c, const fm_attention_args* a,
+                                        void* ws, size_t ws_bytes, fm_stream stream) {
+  FM_TRY(check_attention(c, a));
+  if (!a->cu_rows || !a->kv_len) return set_err(FM_ERR_ARG, "NULL argument");
+  if (!(a->scale > 0.f) || a->scale > 1e30f)
+    return set_err(FM_ERR_ARG, "scale must be finite and > 0");
+  if (c->pos && !a->q_pos) return set_err(FM_ERR_ARG, "a cache with positions needs q_pos");
+  if (a->T == 0) return FM_OK;
+  FM_TRY(check_stride(c, "q", a->q, a->q_stride, a->n_heads, a->T));
+  FM_TRY(check_stride(c, "out", a->out, a->out_stride, a->n_heads, a->T));
+  if (!ws || ((uintptr_t)ws & 255)) return set_err(FM_ERR_ARG, "workspace must be 256-byte aligned");
+  AttnPlan p;
+  FM_TRY(plan_attention(c, a, &p));
+  if (ws_bytes < p.total)
+    return set_err(FM_ERR_ARG, "workspace of %zu bytes, %zu needed", ws_bytes, p.total);
+  fm::CacheAttnArgs k;
+  k.c = view(c);
+  k.T = a->T;
+  k.B = a->B;
+  k.n_heads = a->n_heads;
+  k.G = a->n_heads / c->n_kv_heads;
+  k.max_rows = a->max_rows;
+  k.max_kv = a->max_kv;
+  k.q = a->q;
+  k.qs = a->q_stride;
+  k.os = a->out_stride;
+  k.cu = a->cu_rows;
+  k.kv_len = a->kv_len;
+  k.q_pos = a->q_pos;
+  k.scale_log2 = a->scale * 1.4426950408889634f;
+  k.window = a->window;
+  k.sinks = a->sinks;
+  k.out = a->out;
+  char* w = (char*)ws;
+  k.lse = a->lse ? a->lse : a->accumulate ? (float*)(w + p.o_lse) : nullptr;
+  k.plan_n = (int*)w;
+  k.plan_first = (long long*)(w + p.o_first);
+  k.plan_tile = (int4*)(w + p.o_tile);
+  k.part_ml = (float2*)(w + p.o_ml);
+  k.part = (float*)(w + p.o_part);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (c->dtype == FM_BF16)
+    return c->head_dim == 128 ? run_attention<bf16, 128>(k, p, a->accumulate, st)
+                              : run_attention<bf16, 64>(k, p, a->accumulate, st);
+  if (c->head_dim == 128) return run_attention<float, 128>(k, p, a->accumulate, st);
+  return c->head_dim == 64 ? run_attention<float, 64>(k, p, a->accumulate, st)
+                           : run_attention<float, 32>(k, p, a->accumulate, st);
+}
+
+// ------------------------------------------------------------------ evict
+extern "C" fm_status fm_cache_evict(const fm_paged_cache* c, const int32_t* kv_len,
+                                    const int32_t* next_pos, int B, int max_kv, int budget, int sinks,
+                                    int recent, int32_t* new_len, fm_stream stream) {
+  FM_TRY(check_cache(c));
+  if (!kv_len || !next_pos || !new_len) return set_err(FM_ERR_ARG, "NULL argument");
+  if (!c->pos || !c->weight) return set_err(FM_ERR_ARG, "eviction needs cache->pos and cache->weight");
+  if (B < 1 || max_kv < 1 || budget < 1) return set_err(FM_ERR_ARG, "sizes must be positive");
+  if (B > FM_MAX_CALL_SEQS)
+    return set_err(FM_ERR_UNSUPPORTED, "B=%d exceeds %d sequences", B, FM_MAX_CALL_SEQS);
+  if (max_kv > FM_MAX_EVICT_ROWS)
+    return set_err(FM_ERR_UNSUPPORTED, "max_kv %d exceeds %d", max_kv, FM_MAX_EVICT_ROWS);
+  if (sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
+    return set_err(FM_ERR_ARG, "sinks %d and recent %d must not be negative nor exceed the budget %d",
+                   sinks, recent, budget);
+  if (new_len == kv_len) return set_err(FM_ERR_ARG, "new_len must not be kv_len");
+  fm::EvictArgs k;
+  k.c = view(c);
+  k.kv_len = kv_len;
+  k.next_pos = next_pos;
+  k.new_len = new_len;
+  k.max_kv = max_kv;
+  k.budget = budget;
+  k.sinks = sinks;
+  k.recent = recent;
+  k.row_bytes = c->head_dim * esize(c);
+  // CTAs per (sequence, head): enough that each has at most 4096 rows
+  int C = 1;
+  while (C < fm::EV_MAX_CLUSTER && (max_kv + C - 1) / C > 4096) C *= 2;
+  k.slice_cap = ((max_kv + C - 1) / C + 127) & ~63;
+  static_assert(FM_MAX_EVICT_ROWS <= fm::EV_SLICE * fm::EV_MAX_CLUSTER, "slice");
+  FM_CUDA(fm::set_smem_once(fm::k_cache_evict, fm::evict_smem(fm::EV_SLICE + 128)));
+  FM_LAUNCH_OK("cache evict",
+               fm::launch_pdl_cluster(fm::k_cache_evict, dim3((unsigned)(B * c->n_kv_heads * C)),
+                                      dim3(fm::EV_THREADS), (size_t)fm::evict_smem(k.slice_cap),
+                                      (cudaStream_t)stream, (unsigned)C, k));
+  return FM_OK;
+}

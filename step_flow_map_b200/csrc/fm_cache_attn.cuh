@@ -1,0 +1,464 @@
+// Attention of new rows over the target's paged key/value cache.
+//
+//   s = scale q.k,  p = softmax of s over the rows a query sees,  o = sum p v,
+//   lse = log sum e^s,  weight_r += sum of p over queries and query heads
+//
+// The query heads of one key/value head share its rows, so they are packed:
+// packed row x = i G + j is query i, head g G + j (G query heads per
+// key/value head).  A tile is QT packed rows of one (sequence, key/value
+// head); its unit of work is one block of KB cache rows.  Lengths live on the
+// device (a captured launch serves them as they change), so the split is
+// decided there: all units of all tiles, in order, are dealt to the CTAs in
+// equal runs, whatever the lengths.  A CTA keeps (max, sum, O) over the
+// blocks of a tile that fall in its run and writes the result when it had all
+// of them, else a partial; at most two partials per CTA (its first and its
+// last tile), so the workspace does not grow with the lengths.  A second
+// kernel joins the partials of split tiles in CTA order.
+#pragma once
+#include "fm_cache.cuh"
+
+namespace fm {
+
+struct CacheAttnArgs {
+  CacheView c;
+  int T, B, n_heads, G, max_rows, max_kv;
+  const void* q;
+  int64_t qs, os;
+  const int *cu, *kv_len, *q_pos;
+  float scale_log2;                // scale * log2(e)
+  int window, sinks;
+  void* out;
+  float* lse;                      // or null
+  // workspace
+  int* plan_n;                     // [0]: number of tiles
+  long long* plan_first;           // [tiles + 1]: first unit of each tile, heads apart
+  int4* plan_tile;                 // [tiles][2]: (b, tile, -, -), (s_end, lo, hi, -)
+  float* part;                     // [grid][2][QT][DH]
+  float2* part_ml;                 // [grid][2][QT]: (max, sum), log2 units
+};
+
+// Rows a tile can see: [0, s_end) and [lo, hi), s_end <= lo.
+struct SeenRows {
+  int s_end, lo, hi;
+};
+__device__ __forceinline__ SeenRows seen_rows(const CacheAttnArgs& a, const NewRows& s, int i0,
+                                              int i1) {
+  SeenRows r;
+  const int len = min(s.L, min(a.max_kv, a.c.table_stride << a.c.ps_log2));
+  r.s_end = 0;
+  r.lo = 0;
+  r.hi = len;
+  if (a.c.pos) return r;           // any row may hold any position
+  const long long p0 = (long long)s.L - s.n + i0, p1 = (long long)s.L - s.n + i1;
+  r.hi = (int)max(0ll, min((long long)len, p1 + 1));
+  if (a.window > 0) {
+    r.lo = (int)min((long long)r.hi, max(0ll, p0 - a.window + 1));
+    r.s_end = min(a.sinks, r.lo);
+  }
+  return r;
+}
+// Its blocks of KB rows: nb in all, the j-th at row block_row(j).
+template <int KB>
+struct SeenBlocks {
+  int ns, b0, nb;                  // blocks of [0, s_end), first block of [lo, hi), all
+  __device__ __forceinline__ explicit SeenBlocks(const SeenRows& r) {
+    b0 = r.lo / KB;
+    ns = min((r.s_end + KB - 1) / KB, b0);
+    // a tile that sees nothing still has one (masked) block, which writes its zeros
+    nb = max(1, ns + max(0, (r.hi + KB - 1) / KB - b0));
+  }
+  __device__ __forceinline__ int row(int j) const { return (j < ns ? j : j - ns + b0) * KB; }
+};
+__device__ __forceinline__ bool row_seen(const SeenRows& s, int r) {
+  return r < s.s_end || (r >= s.lo && r < s.hi);
+}
+// The mask of one (query position, row position) pair.  The difference is
+// taken unsigned once the order is known, so no pair of positions overflows.
+__device__ __forceinline__ bool sees(int pq, int pk, int window, int sinks) {
+  return pk <= pq && (window == 0 || (unsigned)pq - (unsigned)pk < (unsigned)window || pk < sinks);
+}
+
+// ------------------------------------------------------------------ plan
+// One CTA lists the tiles of every sequence and prefix-sums their blocks.
+constexpr int CP_THREADS = 1024;
+template <int QT, int KB>
+__global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a) {
+  __shared__ int s_tiles[257];
+  __shared__ long long s_warp[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  if (tid < 256) {
+    int n = 0;
+    if (tid < a.B) n = min(new_rows(a.cu, a.kv_len, tid, a.T).n, a.max_rows);
+    s_tiles[tid + 1] = (n * a.G + QT - 1) / QT;
+  }
+  if (tid == 0) s_tiles[0] = 0;
+  __syncthreads();
+  for (int o = 1; o < 256; o <<= 1) {
+    int v = 0;
+    if (tid < 256 && tid >= o) v = s_tiles[tid + 1 - o];
+    __syncthreads();
+    if (tid < 256) s_tiles[tid + 1] += v;
+    __syncthreads();
+  }
+  const int E = s_tiles[256];
+  long long base = 0;
+  for (int e0 = 0; e0 < E; e0 += CP_THREADS) {
+    const int e = e0 + tid;
+    long long nb = 0;
+    if (e < E) {
+      int b = 0;                   // largest b with s_tiles[b] <= e
+      for (int step = 128; step > 0; step >>= 1)
+        if (s_tiles[b + step] <= e) b += step;
+      const int tile = e - s_tiles[b];
+      const NewRows s = new_rows(a.cu, a.kv_len, b, a.T);
+      const int rows = min(s.n, a.max_rows) * a.G;
+      const SeenRows r = seen_rows(a, s, tile * QT / a.G, (min(rows, (tile + 1) * QT) - 1) / a.G);
+      nb = SeenBlocks<KB>(r).nb;
+      a.plan_tile[2 * e] = make_int4(b, tile, 0, 0);
+      a.plan_tile[2 * e + 1] = make_int4(r.s_end, r.lo, r.hi, 0);
+    }
+    long long x = nb;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    long long add = base, sum = 0;
+    for (int i = 0; i < 32; ++i) {
+      if (i < warp) add += s_warp[i];
+      sum += s_warp[i];
+    }
+    if (e < E) a.plan_first[e] = add + x - nb;
+    base += sum;
+  }
+  if (tid == 0) {
+    a.plan_first[E] = base;
+    a.plan_n[0] = E;
+  }
+}
+
+// The run of units of CTA c of `grid`, and the tile a unit falls in.  Units of
+// a tile: all blocks of head 0, then of head 1, and so on.
+struct WorkRun {
+  long long N;
+  int g;                           // CTAs that have work
+  __device__ __forceinline__ long long start(int c) const { return N * c / g; }
+  __device__ __forceinline__ int cta_of(long long u) const { return (int)(((u + 1) * g - 1) / N); }
+};
+__device__ __forceinline__ WorkRun work_run(const CacheAttnArgs& a, int E, int grid) {
+  WorkRun w;
+  w.N = a.plan_first[E] * a.c.n_kv;
+  w.g = (int)min((long long)grid, w.N);
+  return w;
+}
+// Largest e with plan_first[e] n_kv <= u; every lane of the warp takes part,
+// 32 probes a round.
+__device__ __forceinline__ int find_tile(const CacheAttnArgs& a, int E, long long u) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = E;               // the answer lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lo + lane * step;
+    const bool ok = lane * step < n && a.plan_first[at] * a.c.n_kv <= u;
+    const int k = 31 - __clz((int)__ballot_sync(0xffffffffu, ok));   // lane 0 always holds
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------------ CUDA-core kernel (fp32)
+// Thread grid TR x TC over a tile of QT packed rows and blocks of 64 cache
+// rows; scores, probabilities and O stay fp32.  Bound: FP32 FMA issue for
+// prompts, HBM for few rows (hence the 16-row tile next to the 64-row one).
+constexpr int CS_THREADS = 128;
+constexpr int CS_KB = 64;
+
+template <int DH, int QT>
+struct CsCfg {
+  static constexpr int TC = QT == 64 ? 8 : 16, TR = CS_THREADS / TC;
+  static constexpr int RPT = QT / TR, KPT = CS_KB / TC, CPT = DH / TC;
+  static constexpr int LD = DH + 4, PLD = CS_KB + 4;
+  static constexpr int SMEM = (QT * LD + CS_KB * LD + CS_KB * DH + QT * PLD + 2 * CS_KB) * 4;
+};
+
+template <typename T, int DH, int QT>
+__global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnArgs a) {
+  using C = CsCfg<DH, QT>;
+  constexpr int VE = Vec16<T>::N;
+  constexpr int VW = C::CPT < 4 ? C::CPT : 4;      // neighbouring O columns of a thread
+  extern __shared__ float smf[];
+  float* sq = smf;                                 // [QT][LD]
+  float* sk = sq + QT * C::LD;                     // [KB][LD]
+  float* sv = sk + CS_KB * C::LD;                  // [KB][DH]
+  float* sp = sv + CS_KB * DH;                     // [QT][PLD]
+  int* s_pos = (int*)(sp + QT * C::PLD);           // [KB]
+  int* s_ok = s_pos + CS_KB;                       // [KB]
+  const int tid = threadIdx.x, tr = tid / C::TC, tc = tid % C::TC;
+  pdl_wait();
+  pdl_trigger();
+  const int E = a.plan_n[0];
+  if (E == 0) return;
+  const WorkRun w = work_run(a, E, gridDim.x);
+  if ((int)blockIdx.x >= w.g) return;
+  long long u = w.start(blockIdx.x);
+  const long long u1 = w.start(blockIdx.x + 1);
+  const long long u0 = u;
+  int e = find_tile(a, E, u);
+  while (u < u1) {
+    const long long t0 = a.plan_first[e];
+    const int nb = (int)(a.plan_first[e + 1] - t0);
+    const int g = (int)((u - t0 * a.c.n_kv) / nb), j0 = (int)((u - t0 * a.c.n_kv) % nb);
+    const int j1 = (int)min((long long)nb, j0 + (u1 - u));
+    const int4 pt = a.plan_tile[2 * e], ps = a.plan_tile[2 * e + 1];
+    const int b = pt.x;
+    const SeenRows seen = {ps.x, ps.y, ps.z};
+    const SeenBlocks<CS_KB> blocks(seen);
+    const NewRows s = new_rows(a.cu, a.kv_len, b, a.T);
+    const int x0 = pt.y * QT, rows = min(QT, min(s.n, a.max_rows) * a.G - x0);
+    __syncthreads();
+    for (int i = tid; i < QT * (DH / VE); i += CS_THREADS) {
+      const int r = i / (DH / VE), c = (i % (DH / VE)) * VE;
+      float f[VE];
+      if (r < rows) {
+        const int x = x0 + r;
+        Vec16<T>::unpack(*(const uint4*)((const T*)a.q + (s.first + x / a.G) * a.qs +
+                                         (g * a.G + x % a.G) * DH + c), f);
+      } else {
+#pragma unroll
+        for (int k = 0; k < VE; ++k) f[k] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < VE; ++k) sq[r * C::LD + c + k] = f[k] * a.scale_log2;
+    }
+    int pq[C::RPT];
+    float m[C::RPT], l[C::RPT], o[C::RPT][C::CPT];
+#pragma unroll
+    for (int i = 0; i < C::RPT; ++i) {
+      const int r = tr + C::TR * i;
+      const int qi = (x0 + (r < rows ? r : 0)) / a.G;
+      pq[i] = a.q_pos ? __ldg(a.q_pos + s.first + qi) : s.L - s.n + qi;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < C::CPT; ++c) o[i][c] = 0.f;
+    }
+    for (int j = j0; j < j1; ++j) {
+      const int r0 = blocks.row(j);
+      __syncthreads();
+      for (int i = tid; i < CS_KB * (DH / VE); i += CS_THREADS) {
+        const int r = i / (DH / VE), c = (i % (DH / VE)) * VE, cr = r0 + r;
+        const int page = row_seen(seen, cr) ? cache_page(a.c, b, cr) : -1;
+        float fk[VE], fv[VE];
+#pragma unroll
+        for (int k = 0; k < VE; ++k) fk[k] = fv[k] = 0.f;
+        if (page >= 0) {
+          const size_t at = cache_row(a.c, page, g, cr);
+          Vec16<T>::unpack(*(const uint4*)((const T*)a.c.k + at * DH + c), fk);
+          Vec16<T>::unpack(*(const uint4*)((const T*)a.c.v + at * DH + c), fv);
+          if (c == 0) s_pos[r] = a.c.pos ? a.c.pos[at] : cr;
+        }
+        if (c == 0) s_ok[r] = page >= 0;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+          sk[r * C::LD + c + k] = fk[k];
+          sv[r * DH + c + k] = fv[k];
+        }
+      }
+      __syncthreads();
+      float sc[C::RPT][C::KPT];
+#pragma unroll
+      for (int i = 0; i < C::RPT; ++i)
+#pragma unroll
+        for (int k = 0; k < C::KPT; ++k) sc[i][k] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < DH; d += 4) {
+        float4 qv[C::RPT];
+#pragma unroll
+        for (int i = 0; i < C::RPT; ++i) qv[i] = *(const float4*)(sq + (tr + C::TR * i) * C::LD + d);
+#pragma unroll
+        for (int k = 0; k < C::KPT; ++k) {
+          const float4 kv = *(const float4*)(sk + (tc + C::TC * k) * C::LD + d);
+#pragma unroll
+          for (int i = 0; i < C::RPT; ++i) {
+            sc[i][k] = fmaf(qv[i].x, kv.x, sc[i][k]);
+            sc[i][k] = fmaf(qv[i].y, kv.y, sc[i][k]);
+            sc[i][k] = fmaf(qv[i].z, kv.z, sc[i][k]);
+            sc[i][k] = fmaf(qv[i].w, kv.w, sc[i][k]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < C::RPT; ++i) {
+        float mx = m[i];
+#pragma unroll
+        for (int k = 0; k < C::KPT; ++k) {
+          const int kr = tc + C::TC * k;
+          if (!(s_ok[kr] && sees(pq[i], s_pos[kr], a.window, a.sinks))) sc[i][k] = -INFINITY;
+          mx = fmaxf(mx, sc[i][k]);
+        }
+#pragma unroll
+        for (int d = 1; d < C::TC; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const float corr = exp2f(m[i] - ref);      // 0 while nothing was seen
+        m[i] = mx;
+        l[i] *= corr;
+#pragma unroll
+        for (int c = 0; c < C::CPT; ++c) o[i][c] *= corr;
+#pragma unroll
+        for (int k = 0; k < C::KPT; ++k) {
+          const float p = exp2f(sc[i][k] - ref);
+          l[i] += p;
+          sp[(tr + C::TR * i) * C::PLD + tc + C::TC * k] = p;
+        }
+      }
+      __syncwarp();                                // a row's probabilities come from its own warp
+#pragma unroll 4
+      for (int k = 0; k < CS_KB; ++k) {
+        float pv[C::RPT];
+#pragma unroll
+        for (int i = 0; i < C::RPT; ++i) pv[i] = sp[(tr + C::TR * i) * C::PLD + k];
+#pragma unroll
+        for (int c = 0; c < C::CPT; c += VW) {
+          float vv[VW];
+#pragma unroll
+          for (int z = 0; z < VW; ++z) vv[z] = sv[k * DH + c * C::TC + tc * VW + z];
+#pragma unroll
+          for (int i = 0; i < C::RPT; ++i)
+#pragma unroll
+            for (int z = 0; z < VW; ++z) o[i][c + z] = fmaf(pv[i], vv[z], o[i][c + z]);
+        }
+      }
+      __syncwarp();
+    }
+    const bool whole = j0 == 0 && j1 == nb;
+    const int slot = u == u0 ? 0 : 1;
+#pragma unroll
+    for (int i = 0; i < C::RPT; ++i) {
+#pragma unroll
+      for (int d = 1; d < C::TC; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+      const int r = tr + C::TR * i;
+      if (r >= rows) continue;
+      if (whole) {
+        const int x = x0 + r, t = s.first + x / a.G, h = g * a.G + x % a.G;
+        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+        T* dst = (T*)a.out + t * a.os + h * DH;
+#pragma unroll
+        for (int c = 0; c < C::CPT; ++c)
+          dst[(c / VW) * VW * C::TC + tc * VW + c % VW] = from_f<T>(o[i][c] * inv);
+        if (a.lse && tc == 0)
+          a.lse[(size_t)t * a.n_heads + h] =
+              l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
+      } else {
+        const size_t p = ((size_t)blockIdx.x * 2 + slot) * QT + r;
+#pragma unroll
+        for (int c = 0; c < C::CPT; ++c)
+          a.part[p * DH + (c / VW) * VW * C::TC + tc * VW + c % VW] = o[i][c];
+        if (tc == 0) a.part_ml[p] = make_float2(m[i], l[i]);
+      }
+    }
+    u += j1 - j0;
+    if (u - t0 * a.c.n_kv >= (long long)nb * a.c.n_kv) ++e;
+  }
+}
+
+// ------------------------------------------------------------------ join
+// The partials of a split tile, one warp per packed row.  CTA x looks at the
+// start of run x: it joins the tile that run x - 1 began and left, unless an
+// earlier boundary already fell in that tile.
+constexpr int CJ_THREADS = 128;
+template <typename T, int DH, int QT>
+__global__ void __launch_bounds__(CJ_THREADS) k_cache_join(const CacheAttnArgs a, int grid) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int c = blockIdx.x + 1;
+  const int E = a.plan_n[0];
+  if (E == 0) return;
+  const WorkRun w = work_run(a, E, grid);
+  if (c >= w.g) return;
+  const long long u = w.start(c);
+  const int e = find_tile(a, E, u);
+  const long long t0 = a.plan_first[e];
+  const int nb = (int)(a.plan_first[e + 1] - t0);
+  const int g = (int)((u - t0 * a.c.n_kv) / nb);
+  const long long first = t0 * a.c.n_kv + (long long)g * nb;
+  if (first == u || w.start(c - 1) > first) return;
+  const int last = w.cta_of(first + nb - 1);
+  const int4 pt = a.plan_tile[2 * e];
+  const NewRows s = new_rows(a.cu, a.kv_len, pt.x, a.T);
+  const int r = blockIdx.y * (CJ_THREADS / 32) + (threadIdx.x >> 5);
+  const int x = pt.y * QT + r;
+  if (r >= QT || x >= min(s.n, a.max_rows) * a.G) return;
+  const int slot0 = w.start(c - 1) == first ? 0 : 1;   // run c - 1 began the tile
+  auto at = [&](int i) { return ((size_t)i * 2 + (i == c - 1 ? slot0 : 0)) * QT + r; };
+  float m = -INFINITY;
+  for (int i = c - 1 + lane; i <= last; i += 32) m = fmaxf(m, a.part_ml[at(i)].x);
+  m = warp_max(m);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[DH / 32];
+#pragma unroll
+  for (int k = 0; k < DH / 32; ++k) o[k] = 0.f;
+#pragma unroll 4
+  for (int i = c - 1; i <= last; ++i) {
+    const size_t p = at(i);
+    const float2 ml = a.part_ml[p];
+    const float f = exp2f(ml.x - ref);
+    l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int k = 0; k < DH / 32; ++k) o[k] = fmaf(a.part[p * DH + lane + 32 * k], f, o[k]);
+  }
+  const int t = s.first + x / a.G, h = g * a.G + x % a.G;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int k = 0; k < DH / 32; ++k)
+    ((T*)a.out)[t * a.os + h * DH + lane + 32 * k] = from_f<T>(o[k] * inv);
+  if (a.lse && lane == 0)
+    a.lse[(size_t)t * a.n_heads + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// ------------------------------------------------------------------ weights
+// weight_r += sum over queries and heads of e^(s - lse): one warp per cache
+// row, the key in registers, the queries in order (no atomics, so the sum
+// does not depend on scheduling).
+constexpr int CW_THREADS = 256;
+template <typename T, int DH>
+__global__ void __launch_bounds__(CW_THREADS) k_cache_weights(const CacheAttnArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, g = blockIdx.y, b = blockIdx.z;
+  const NewRows s = new_rows(a.cu, a.kv_len, b, a.T);
+  const int n = min(s.n, a.max_rows);
+  if (n == 0) return;
+  const SeenRows seen = seen_rows(a, s, 0, n - 1);
+  for (int r = blockIdx.x * (CW_THREADS / 32) + (threadIdx.x >> 5); r < seen.hi;
+       r += gridDim.x * (CW_THREADS / 32)) {
+    const int page = row_seen(seen, r) ? cache_page(a.c, b, r) : -1;
+    if (page < 0) continue;
+    const size_t at = cache_row(a.c, page, g, r);
+    const int pk = a.c.pos ? a.c.pos[at] : r;
+    float kv[DH / 32];
+#pragma unroll
+    for (int k = 0; k < DH / 32; ++k) kv[k] = to_f(((const T*)a.c.k)[at * DH + lane + 32 * k]);
+    float sum = 0.f;
+    for (int x = 0; x < n * a.G; ++x) {
+      const int t = s.first + x / a.G, h = g * a.G + x % a.G;
+      const int pq = a.q_pos ? __ldg(a.q_pos + t) : s.L - s.n + x / a.G;
+      if (!sees(pq, pk, a.window, a.sinks)) continue;
+      float d = 0.f;
+#pragma unroll
+      for (int k = 0; k < DH / 32; ++k)
+        d = fmaf(to_f(((const T*)a.q)[t * a.qs + h * DH + lane + 32 * k]), kv[k], d);
+      d = warp_sum(d);
+      sum += exp2f(d * a.scale_log2 - a.lse[(size_t)t * a.n_heads + h] * 1.4426950408889634f);
+    }
+    if (lane == 0) a.c.weight[at] += sum;
+  }
+}
+
+}  // namespace fm

@@ -9,8 +9,10 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (FM_BF16, FM_F32, fm_draft, fm_draft_factorised, fm_free, fm_load_weights,
-               fm_project_context, fm_verify_greedy, fm_verify_sample)
+from . import (FM_BF16, FM_F32, fm_append_args, fm_attention_args, fm_cache_append,
+               fm_cache_attention, fm_cache_attention_workspace, fm_cache_evict, fm_draft,
+               fm_draft_factorised, fm_free, fm_load_weights, fm_paged_cache, fm_project_context,
+               fm_verify_greedy, fm_verify_sample)
 
 TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
 FM_DTYPE = {"f32": FM_F32, "bf16": FM_BF16}
@@ -98,3 +100,164 @@ class Context:
         fm_verify_sample(self.ctx, target, draft_logits, draft, B, N, K1 - 1, V, T, u_accept,
                          u_res, n, br, out, stream)
         return n, br, out
+
+
+class PagedCache:
+    """One layer of the target's paged key/value cache: torch tensors in the
+    library's layout, and the operators that work on them (argument checks and
+    marshalling only; see the C header for every argument's meaning).
+
+    k, v [n_pages, n_kv_heads, page_size, head_dim] (bf16 or fp32), page_table
+    [n_seqs, table_stride] int32, pos [n_pages, n_kv_heads, page_size] int32 or
+    None, weight (same shape) fp32 or None; all contiguous, on one GPU.  The
+    tensors may be changed in place between calls; `page_table` may be
+    replaced.
+
+    Calls run on `stream`, or on the current stream of the cache's device;
+    outputs and workspaces are allocated on that stream, one workspace per
+    call, so calls on different streams (or captured in different graphs)
+    share nothing but what they are given.
+    """
+
+    def __init__(self, k, v, page_table, pos=None, weight=None):
+        if k.dtype not in (torch.bfloat16, torch.float32) or k.dim() != 4:
+            raise ValueError("k must be [n_pages, n_kv_heads, page_size, head_dim], bf16 or fp32")
+        self.k, self.v, self.pos, self.weight = k, v, pos, weight
+        self.device = k.device
+        n_pages, n_kv, ps, dh = k.shape
+        self._check("v", v, k.dtype, k.shape)
+        for name, t, dt in (("pos", pos, torch.int32), ("weight", weight, torch.float32)):
+            if t is not None:
+                self._check(name, t, dt, k.shape[:3])
+        if not k.is_contiguous():
+            raise ValueError("k must be contiguous")
+        self._c = fm_paged_cache(
+            dtype=FM_BF16 if k.dtype == torch.bfloat16 else FM_F32, n_pages=n_pages, page_size=ps,
+            n_kv_heads=n_kv, head_dim=dh, k=k.data_ptr(), v=v.data_ptr(),
+            pos=pos.data_ptr() if pos is not None else None,
+            weight=weight.data_ptr() if weight is not None else None)
+        self.page_table = page_table
+
+    @property
+    def page_table(self):
+        return self._table
+
+    @page_table.setter
+    def page_table(self, t):
+        if t.dim() != 2:
+            raise ValueError("page_table must be [n_seqs, table_stride]")
+        self._check("page_table", t, torch.int32, t.shape)
+        self._table = t
+        self._c.page_table, self._c.table_stride = t.data_ptr(), t.shape[1]
+
+    def _check(self, name, t, dtype, shape):
+        if t.device != self.device or t.dtype != dtype or tuple(t.shape) != tuple(shape) \
+                or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                             f"on {self.device}")
+
+    def _rows(self, name, t, heads):
+        """Row stride of a [T, heads, head_dim] tensor whose heads are contiguous."""
+        dh = self._c.head_dim
+        if t.dim() != 3 or t.shape[2] != dh or (heads and t.shape[1] != heads) \
+                or t.dtype != self.k.dtype or t.device != self.device \
+                or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dh))):
+            raise ValueError(f"{name} must be [T, heads, {dh}] {self.k.dtype} on {self.device} "
+                             "with contiguous heads")
+        # one row's stride says nothing; any aligned one will do
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dh
+
+    def _seqs(self, T, cu_rows, kv_len, q_pos):
+        B = kv_len.shape[0]
+        self._check("kv_len", kv_len, torch.int32, (B,))
+        self._check("cu_rows", cu_rows, torch.int32, (B + 1,))
+        if B > self._table.shape[0]:
+            raise ValueError(f"{B} sequences, {self._table.shape[0]} rows of page_table")
+        if q_pos is not None:
+            self._check("q_pos", q_pos, torch.int32, (T,))
+        return B
+
+    def _on(self, stream):
+        """(context that makes `stream` current on the cache's device, the stream)."""
+        if stream is None:
+            with torch.cuda.device(self.device):
+                stream = torch.cuda.current_stream()
+        elif isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        return torch.cuda.stream(stream), stream
+
+    def append(self, q, k, v, cu_rows, kv_len, q_pos=None, *, q_gain=None, k_gain=None, eps=1e-6,
+               inv_freq=None, interleaved=False, out=None, stream=None):
+        """Norms, rotates and appends the new rows; returns the queries [T, n_heads, head_dim]."""
+        n_kv, dh = self._c.n_kv_heads, self._c.head_dim
+        T, n_heads = q.shape[0], q.shape[1]
+        qs, ks, vs = self._rows("q", q, 0), self._rows("k", k, n_kv), self._rows("v", v, n_kv)
+        if k.shape[0] != T or v.shape[0] != T:
+            raise ValueError("q, k and v must have the same rows")
+        B = self._seqs(T, cu_rows, kv_len, q_pos)
+        for name, g in (("q_gain", q_gain), ("k_gain", k_gain)):
+            if g is not None:
+                self._check(name, g, self.k.dtype, (dh,))
+        rot = 0
+        if inv_freq is not None:
+            rot = 2 * inv_freq.shape[0]
+            self._check("inv_freq", inv_freq, torch.float64, (rot // 2,))
+        ctx, st = self._on(stream)
+        with ctx:
+            if out is None:
+                out = torch.empty((T, n_heads, dh), dtype=q.dtype, device=self.device)
+            elif out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+            fm_cache_append(self._c, fm_append_args(
+                T=T, B=B, n_heads=n_heads, q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(),
+                q_stride=qs, k_stride=ks, v_stride=vs,
+                q_gain=q_gain.data_ptr() if q_gain is not None else None,
+                k_gain=k_gain.data_ptr() if k_gain is not None else None, eps=eps,
+                inv_freq=inv_freq.data_ptr() if rot else None, rot_dim=rot,
+                interleaved=int(bool(interleaved)), cu_rows=cu_rows.data_ptr(),
+                kv_len=kv_len.data_ptr(), q_pos=q_pos.data_ptr() if q_pos is not None else None,
+                q_out=out.data_ptr(), q_out_stride=self._rows("out", out, n_heads)), st)
+        return out
+
+    def attend(self, q, cu_rows, kv_len, *, max_rows, max_kv, q_pos=None, scale=None, window=0,
+               sinks=0, accumulate=False, lse=False, out=None, stream=None):
+        """Attention of the new rows; returns out, or (out, lse) with ``lse=True``."""
+        T, n_heads = q.shape[0], q.shape[1]
+        qs = self._rows("q", q, 0)
+        B = self._seqs(T, cu_rows, kv_len, q_pos)
+        ctx, st = self._on(stream)
+        with ctx:
+            if out is None:
+                out = torch.empty((T, n_heads, q.shape[2]), dtype=q.dtype, device=self.device)
+            elif out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+            got = torch.empty((T, n_heads), dtype=torch.float32, device=self.device) if lse else None
+            a = fm_attention_args(
+                T=T, B=B, n_heads=n_heads, max_rows=max_rows, max_kv=max_kv, q=q.data_ptr(),
+                q_stride=qs, cu_rows=cu_rows.data_ptr(), kv_len=kv_len.data_ptr(),
+                q_pos=q_pos.data_ptr() if q_pos is not None else None,
+                scale=scale if scale is not None else q.shape[2] ** -0.5, window=window, sinks=sinks,
+                accumulate=int(bool(accumulate)), out=out.data_ptr(),
+                out_stride=self._rows("out", out, n_heads),
+                lse=got.data_ptr() if lse else None)
+            ws_bytes = fm_cache_attention_workspace(self._c, a)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device)
+            fm_cache_attention(self._c, a, ws, ws_bytes, st)
+        return (out, got) if lse else out
+
+    def evict(self, kv_len, next_pos, budget, *, max_kv, sinks=0, recent=0, new_len=None,
+              stream=None):
+        """Cuts every (sequence, head) to `budget` rows in place; returns the new lengths [B]."""
+        B = kv_len.shape[0]
+        self._check("kv_len", kv_len, torch.int32, (B,))
+        self._check("next_pos", next_pos, torch.int32, (B,))
+        if B > self._table.shape[0]:
+            raise ValueError(f"{B} sequences, {self._table.shape[0]} rows of page_table")
+        ctx, st = self._on(stream)
+        with ctx:
+            if new_len is None:
+                new_len = torch.empty_like(kv_len)
+            else:
+                self._check("new_len", new_len, torch.int32, (B,))
+            fm_cache_evict(self._c, kv_len, next_pos, B, max_kv, budget, sinks, recent, new_len, st)
+        return new_len
