@@ -10,6 +10,7 @@
 #include "fm_host.cuh"
 #include "fm_cache.cuh"
 #include "fm_cache_attn.cuh"
+#include "fm_cache_decode.cuh"
 
 using fm::bf16;
 
@@ -36,9 +37,9 @@ fm_status check_cache(const fm_paged_cache* c) {
       c->table_stride > MAX_ROWS / c->page_size)
     return set_err(FM_ERR_UNSUPPORTED, "cache too large: pages x heads x page_size must stay below "
                    "2^31, table_stride x page_size at most 2^24");
-  if (!aligned16(c->k) || !aligned16(c->v) || ((uintptr_t)c->pos & 3) || ((uintptr_t)c->weight & 3) ||
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->pos) || ((uintptr_t)c->weight & 3) ||
       ((uintptr_t)c->page_table & 3))
-    return set_err(FM_ERR_ARG, "k and v must be 16-byte aligned, pos, weight and page_table 4-byte");
+    return set_err(FM_ERR_ARG, "k, v and pos must be 16-byte aligned, weight and page_table 4-byte");
   return FM_OK;
 }
 
@@ -173,6 +174,7 @@ namespace {
 
 // What a call runs and where its workspace parts lie.
 struct AttnPlan {
+  bool decode = false;             // k_cache_decode: bf16, at most 16 packed rows
   int qt = 0, grid = 0;
   int64_t tiles = 0;
   size_t o_first = 0, o_tile = 0, o_lse = 0, o_ml = 0, o_part = 0, total = 0;
@@ -197,6 +199,7 @@ fm_status plan_attention(const fm_paged_cache* c, const fm_attention_args* a, At
   FM_TRY(device_sms(&sms));
   const int64_t G = a->n_heads / c->n_kv_heads;
   p->qt = a->max_rows * G <= 16 ? 16 : 64;
+  p->decode = c->dtype == FM_BF16 && p->qt == 16;
   p->grid = 2 * sms;
   p->tiles = ((int64_t)a->T * G) / p->qt + a->B;
   size_t at = 256;
@@ -228,10 +231,30 @@ fm_status launch_simt(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_
   return FM_OK;
 }
 
+template <int DH>
+fm_status launch_decode(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_t st) {
+  using C = fm::CdCfg<DH>;
+  FM_CUDA(fm::set_smem_once(fm::k_cache_decode<DH>, C::SMEM));
+  // no more CTAs than units
+  const int64_t units = (int64_t)k.B * k.c.n_kv * ((k.max_kv + fm::CD_KB - 1) / fm::CD_KB + 1);
+  const int grid = (int)std::min<int64_t>(p.grid, units);
+  FM_LAUNCH_OK("cache attention", fm::launch_pdl(fm::k_cache_decode<DH>, dim3(grid),
+                                                 dim3(fm::CD_THREADS), C::SMEM, st, k));
+  if (grid > 1)
+    FM_LAUNCH_OK("cache attention join",
+                 fm::launch_pdl(fm::k_cache_decode_join<DH>,
+                                dim3(grid - 1, (unsigned)((k.max_rows * k.G + 3) / 4)),
+                                dim3(fm::CD_THREADS), 0, st, k, grid));
+  return FM_OK;
+}
+
 template <typename T, int DH>
 fm_status run_attention(const fm::CacheAttnArgs& k, const AttnPlan& p, int accumulate,
                         cudaStream_t st) {
-  if (p.qt == 16) FM_TRY((launch_simt<T, DH, 16>(k, p, st)));
+  if constexpr (std::is_same<T, bf16>::value) {
+    if (p.decode) FM_TRY(launch_decode<DH>(k, p, st));
+    else FM_TRY((launch_simt<T, DH, 64>(k, p, st)));
+  } else if (p.qt == 16) FM_TRY((launch_simt<T, DH, 16>(k, p, st)));
   else FM_TRY((launch_simt<T, DH, 64>(k, p, st)));
   if (accumulate) {
     const int per = fm::CW_THREADS / 32;

@@ -372,11 +372,41 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
 // start of run x: it joins the tile that run x - 1 began and left, unless an
 // earlier boundary already fell in that tile.
 constexpr int CJ_THREADS = 128;
+// Row x of a tile whose partials are runs c0 .. last (run c0's in slot slot0,
+// the others' in slot 0), one warp, to output row t and head h.
+template <typename T, int DH>
+__device__ __forceinline__ void join_row(const CacheAttnArgs& a, int c0, int last, int slot0, int qt,
+                                         int x, int t, int h) {
+  const int lane = threadIdx.x & 31;
+  auto at = [&](int i) { return ((size_t)i * 2 + (i == c0 ? slot0 : 0)) * qt + x; };
+  float m = -INFINITY;
+  for (int i = c0 + lane; i <= last; i += 32) m = fmaxf(m, a.part_ml[at(i)].x);
+  m = warp_max(m);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[DH / 32];
+#pragma unroll
+  for (int k = 0; k < DH / 32; ++k) o[k] = 0.f;
+#pragma unroll 8
+  for (int i = c0; i <= last; ++i) {
+    const size_t p = at(i);
+    const float2 ml = a.part_ml[p];
+    const float f = exp2f(ml.x - ref);
+    l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int k = 0; k < DH / 32; ++k) o[k] = fmaf(a.part[p * DH + lane + 32 * k], f, o[k]);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int k = 0; k < DH / 32; ++k)
+    ((T*)a.out)[t * a.os + h * DH + lane + 32 * k] = from_f<T>(o[k] * inv);
+  if (a.lse && lane == 0)
+    a.lse[(size_t)t * a.n_heads + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
 template <typename T, int DH, int QT>
 __global__ void __launch_bounds__(CJ_THREADS) k_cache_join(const CacheAttnArgs a, int grid) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
   const int c = blockIdx.x + 1;
   const int E = a.plan_n[0];
   if (E == 0) return;
@@ -395,31 +425,9 @@ __global__ void __launch_bounds__(CJ_THREADS) k_cache_join(const CacheAttnArgs a
   const int r = blockIdx.y * (CJ_THREADS / 32) + (threadIdx.x >> 5);
   const int x = pt.y * QT + r;
   if (r >= QT || x >= min(s.n, a.max_rows) * a.G) return;
-  const int slot0 = w.start(c - 1) == first ? 0 : 1;   // run c - 1 began the tile
-  auto at = [&](int i) { return ((size_t)i * 2 + (i == c - 1 ? slot0 : 0)) * QT + r; };
-  float m = -INFINITY;
-  for (int i = c - 1 + lane; i <= last; i += 32) m = fmaxf(m, a.part_ml[at(i)].x);
-  m = warp_max(m);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[DH / 32];
-#pragma unroll
-  for (int k = 0; k < DH / 32; ++k) o[k] = 0.f;
-#pragma unroll 4
-  for (int i = c - 1; i <= last; ++i) {
-    const size_t p = at(i);
-    const float2 ml = a.part_ml[p];
-    const float f = exp2f(ml.x - ref);
-    l = fmaf(ml.y, f, l);
-#pragma unroll
-    for (int k = 0; k < DH / 32; ++k) o[k] = fmaf(a.part[p * DH + lane + 32 * k], f, o[k]);
-  }
-  const int t = s.first + x / a.G, h = g * a.G + x % a.G;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int k = 0; k < DH / 32; ++k)
-    ((T*)a.out)[t * a.os + h * DH + lane + 32 * k] = from_f<T>(o[k] * inv);
-  if (a.lse && lane == 0)
-    a.lse[(size_t)t * a.n_heads + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  // run c - 1 began the tile
+  join_row<T, DH>(a, c - 1, last, w.start(c - 1) == first ? 0 : 1, QT, r, s.first + x / a.G,
+                  g * a.G + x % a.G);
 }
 
 // ------------------------------------------------------------------ weights
