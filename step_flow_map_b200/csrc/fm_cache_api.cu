@@ -11,6 +11,7 @@
 #include "fm_cache.cuh"
 #include "fm_cache_attn.cuh"
 #include "fm_cache_decode.cuh"
+#include "fm_cache_tc.cuh"
 
 using fm::bf16;
 
@@ -174,7 +175,10 @@ namespace {
 
 // What a call runs and where its workspace parts lie.
 struct AttnPlan {
-  bool decode = false;             // k_cache_decode: bf16, at most 16 packed rows
+  // bf16: k_cache_decode up to 16 packed rows of a key/value head (its MMA's
+  // M), else k_cache_attn_tc, in pairs of 128-row tiles past 128 rows; fp32:
+  // k_cache_attn_simt with 16- or 64-row tiles
+  enum { DECODE, TC_ONE, TC_PAIR, SIMT } kind = SIMT;
   int qt = 0, grid = 0;
   int64_t tiles = 0;
   size_t o_first = 0, o_tile = 0, o_lse = 0, o_ml = 0, o_part = 0, total = 0;
@@ -198,9 +202,16 @@ fm_status plan_attention(const fm_paged_cache* c, const fm_attention_args* a, At
   int sms = 0;
   FM_TRY(device_sms(&sms));
   const int64_t G = a->n_heads / c->n_kv_heads;
-  p->qt = a->max_rows * G <= 16 ? 16 : 64;
-  p->decode = c->dtype == FM_BF16 && p->qt == 16;
+  const int64_t rows = a->max_rows * G;
+  p->qt = rows <= 16 ? 16 : 64;
   p->grid = 2 * sms;
+  if (c->dtype == FM_BF16) {
+    p->kind = rows <= 16 ? AttnPlan::DECODE : rows <= 128 ? AttnPlan::TC_ONE : AttnPlan::TC_PAIR;
+    if (rows > 16) {
+      p->qt = rows <= 128 ? 128 : 256;
+      p->grid = sms;
+    }
+  }
   p->tiles = ((int64_t)a->T * G) / p->qt + a->B;
   size_t at = 256;
   p->o_first = at;
@@ -248,12 +259,46 @@ fm_status launch_decode(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStrea
   return FM_OK;
 }
 
+template <int DH, bool PAIR>
+fm_status launch_tc(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_t st) {
+  using C = fm::CtCfg<DH>;
+  constexpr int QT = PAIR ? 256 : 128;
+  auto kernel = fm::k_cache_attn_tc<DH, PAIR>;
+  char err[256] = "";
+  auto enc = fm::tma_encoder(err, sizeof(err));
+  if (!enc) return set_err(FM_ERR_CUDA, "%s", err);
+  // one row of the map is one cached row of one head; a box is 64 columns of
+  // the part of a page that one block of 128 rows takes
+  CUtensorMap mk, mv;
+  const cuuint64_t dims[2] = {(cuuint64_t)DH, ((cuuint64_t)k.c.n_pages * k.c.n_kv) << k.c.ps_log2};
+  const cuuint64_t strides[1] = {(cuuint64_t)DH * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)(1 << k.c.ps_log2)};
+  const cuuint32_t es[2] = {1, 1};
+  for (int i = 0; i < 2; ++i) {
+    const CUresult r = enc(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, i ? k.c.v : k.c.k, dims,
+                           strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return set_err(FM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  }
+  FM_CUDA(fm::set_smem_once(kernel, C::SMEM));
+  FM_LAUNCH_OK("cache attention plan",
+               fm::launch_pdl(fm::k_cache_plan<QT, fm::CT_KB>, dim3(1), dim3(fm::CP_THREADS), 0, st, k));
+  FM_LAUNCH_OK("cache attention", fm::launch_pdl(kernel, dim3(p.grid), dim3(fm::CT_THREADS), C::SMEM,
+                                                 st, mk, mv, k));
+  FM_LAUNCH_OK("cache attention join",
+               fm::launch_pdl(fm::k_cache_join<bf16, DH, QT>, dim3(p.grid - 1, QT / 4),
+                              dim3(fm::CJ_THREADS), 0, st, k, p.grid));
+  return FM_OK;
+}
+
 template <typename T, int DH>
 fm_status run_attention(const fm::CacheAttnArgs& k, const AttnPlan& p, int accumulate,
                         cudaStream_t st) {
   if constexpr (std::is_same<T, bf16>::value) {
-    if (p.decode) FM_TRY(launch_decode<DH>(k, p, st));
-    else FM_TRY((launch_simt<T, DH, 64>(k, p, st)));
+    if (p.kind == AttnPlan::DECODE) FM_TRY(launch_decode<DH>(k, p, st));
+    else if (p.kind == AttnPlan::TC_ONE) FM_TRY((launch_tc<DH, false>(k, p, st)));
+    else FM_TRY((launch_tc<DH, true>(k, p, st)));
   } else if (p.qt == 16) FM_TRY((launch_simt<T, DH, 16>(k, p, st)));
   else FM_TRY((launch_simt<T, DH, 64>(k, p, st)));
   if (accumulate) {

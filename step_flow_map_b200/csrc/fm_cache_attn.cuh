@@ -30,7 +30,7 @@ struct CacheAttnArgs {
   void* out;
   float* lse;                      // or null
   // workspace
-  int* plan_n;                     // [0]: number of tiles
+  int* plan_n;                     // [0]: number of tiles, [1]: status of the call
   long long* plan_first;           // [tiles + 1]: first unit of each tile, heads apart
   int4* plan_tile;                 // [tiles][2]: (b, tile, -, -), (s_end, lo, hi, -)
   float* part;                     // [grid][2][QT][DH]
@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a
   if (tid == 0) {
     a.plan_first[E] = base;
     a.plan_n[0] = E;
+    a.plan_n[1] = 0;
   }
 }
 

@@ -117,12 +117,6 @@ __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, boo
                "r"(live ? 16u : 0u)
                : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 template <int DH>
 __global__ void __launch_bounds__(CD_THREADS, 2) k_cache_decode(const CacheAttnArgs a) {
   using C = CdCfg<DH>;
@@ -134,6 +128,7 @@ __global__ void __launch_bounds__(CD_THREADS, 2) k_cache_decode(const CacheAttnA
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0 && tid == 0) a.plan_n[1] = 0;
   decode_scan<CD_KB>(a, s, s_scan);
   const WorkRun w = decode_run(a, s, gridDim.x);
   if ((int)blockIdx.x >= w.g) return;

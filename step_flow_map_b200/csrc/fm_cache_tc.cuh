@@ -1,0 +1,448 @@
+// Attention of many new rows over the paged cache (bf16, more than 16 packed
+// rows per key/value head: drafted blocks, prompts) on tcgen05.
+//
+// Per block of 128 cache rows: S = Q K^T (128 packed rows x 128 keys, fp32 in
+// TMEM), P = 2^(S - m) rounded to bf16 over S's own columns, O += P V with P
+// read from TMEM.  Keys and values come page by page through TMA into a ring
+// of 128-row tiles (128-byte swizzle): K as the K-major operand, V as it lies,
+// MN-major.  Two softmax warpgroups, one thread per packed row, work on two
+// S/O pairs that fill TMEM (2 x (128 + DH) columns), so one's exponentials run
+// under the other's products:
+//   PAIR  (more than 128 packed rows) the pairs are two tiles of 128 rows that
+//         share every K/V tile;
+//   else  one tile of 128 rows: even blocks go to pair 0, odd ones to pair 1,
+//         merged at the end of the tile.
+// Bound: for prompts the exponentials (16 a clock and SM) and the products
+// about equally; for drafted blocks HBM.
+//
+// Roles (384 threads): warp 0 TMA, warp 1 MMA, warps 4-7 and 8-11 softmax.
+// O is rescaled by the softmax threads, and only when a row maximum has grown
+// by more than 2^8 since the reference in use: p stays below 2^8, which costs
+// no precision in bf16 or fp32.  Every wait is bounded; a thread whose wait
+// gave up goes on through the same barriers (later waits end at once) and the
+// workspace's status word is set.
+#pragma once
+#include "fm_cache_attn.cuh"
+#include "fm_ptx.cuh"
+
+namespace fm {
+
+constexpr int CT_THREADS = 384;
+constexpr int CT_KB = 128;
+constexpr int CT_ERR_TIMEOUT = 1;
+
+template <int DH>
+struct CtCfg {
+  static constexpr int TILE = 128 * DH * 2;            // 128 rows of Q, K or V
+  static constexpr int BOX = 128 * 128;                // its 64-column half
+  static constexpr int STAGES = DH == 128 ? 5 : 8;
+  static constexpr int O_COL = 256;                    // TMEM: S0, S1 (128 each), O0, O1
+  static constexpr int BARS = 2 * STAGES + 7;          // full, empty, s_full, p_full, o_full, q_full
+  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + 2 * 128 * 4 + 256;
+};
+
+// A stretch of one tile's blocks inside a CTA's run.
+struct TileSeg {
+  int e, g, j0, n, nb, b, x0;
+  SeenRows seen;
+  __device__ __forceinline__ void at(const CacheAttnArgs& a, int qt, long long u, long long u1) {
+    const long long t0 = a.plan_first[e];
+    nb = (int)(a.plan_first[e + 1] - t0);
+    const long long d = u - t0 * a.c.n_kv;
+    g = (int)(d / nb);
+    j0 = (int)(d - (long long)g * nb);
+    n = (int)min((long long)(nb - j0), u1 - u);
+    const int4 t = a.plan_tile[2 * e], s = a.plan_tile[2 * e + 1];
+    b = t.x;
+    x0 = t.y * qt;
+    seen.s_end = s.x;
+    seen.lo = s.y;
+    seen.hi = s.z;
+  }
+  __device__ __forceinline__ void done(const CacheAttnArgs& a) {
+    if (j0 + n == nb && g + 1 == a.c.n_kv) ++e;
+  }
+};
+
+template <int DH, bool PAIR>
+__global__ void __launch_bounds__(CT_THREADS, 1)
+k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                const CacheAttnArgs a) {
+  using C = CtCfg<DH>;
+  constexpr int QT = PAIR ? 256 : 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sQ = base;                                  // two tiles; the second is the merge
+  uint8_t* sKV = base + 2 * C::TILE;                   //   buffer when there is one Q tile
+  int* s_kpos = (int*)(sKV + C::STAGES * C::TILE);     // [2][128] key positions
+  uint64_t* bars = (uint64_t*)(s_kpos + 256);
+  uint64_t *full = bars, *empty = bars + C::STAGES, *s_full = empty + C::STAGES,
+           *p_full = s_full + 2, *o_full = p_full + 2, *q_full = o_full + 2;
+  uint32_t* tmem_slot = (uint32_t*)(bars + C::BARS);
+  volatile int* abort = (volatile int*)(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), 128);
+      mbar_init(smem_u32(&o_full[i]), 1);
+    }
+    mbar_init(smem_u32(q_full), 256);
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  const int E = a.plan_n[0];
+  WorkRun w = {0, 0};
+  if (E > 0) w = work_run(a, E, gridDim.x);
+  const bool active = (int)blockIdx.x < w.g;
+  const long long u0 = active ? w.start(blockIdx.x) : 0;
+  const long long u1 = active ? w.start(blockIdx.x + 1) : 0;
+  TileSeg seg;
+  seg.e = active && warp != 2 && warp != 3 ? find_tile(a, E, u0) : 0;
+
+  if (warp == 0) {
+    // ---------------- TMA producer: lane i takes the block's i-th page
+    const int np = CT_KB >> a.c.ps_log2, ps = 1 << a.c.ps_log2;
+    const int gone = a.c.n_pages * a.c.n_kv * ps;      // past the last row: reads zeros
+    int cnt = 0;
+    bool go = true;                                    // the same in every lane
+    for (long long u = u0; u < u1 && go; u += seg.n) {
+      seg.at(a, QT, u, u1);
+      const SeenBlocks<CT_KB> blocks(seg.seen);
+      for (int j = 0; j < seg.n && go; ++j) {
+        const int r = blocks.row(seg.j0 + j) + lane * ps;
+        int row = gone;
+        if (lane < np && (r < seg.seen.s_end || (r + ps > seg.seen.lo && r < seg.seen.hi))) {
+          const int page = cache_page(a.c, seg.b, r);
+          if (page >= 0) row = (page * a.c.n_kv + seg.g) << a.c.ps_log2;
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++cnt) {
+          const int st = cnt % C::STAGES;
+          const bool ok = go && mbar_wait(smem_u32(&empty[st]), ((cnt / C::STAGES) & 1) ^ 1, abort);
+          go = __all_sync(0xffffffffu, ok);
+          if (!go) continue;
+          const uint32_t fb = smem_u32(&full[st]);
+          if (lane == 0) mbar_expect_tx(fb, C::TILE);
+          __syncwarp();
+          if (lane < np)
+#pragma unroll
+            for (int h = 0; h < DH / 64; ++h)
+              tma_load_2d(smem_u32(sKV + st * C::TILE + h * C::BOX + lane * ps * 128),
+                          kv ? &mapV : &mapK, h * 64, row, fb);
+        }
+        __syncwarp();
+      }
+      seg.done(a);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer.  Step s of a segment: PAIR: block s/2 for
+    // pair s%2; else block s for pair s%2.  S runs two steps ahead of PV, and
+    // S of a pair is issued after the PV that reads the P it overwrites.
+    constexpr uint32_t idS = idesc_bf16<128>();
+    constexpr uint32_t idO = idesc_bf16<DH>() | (1u << 16);   // V: MN-major
+    int cnt = 0, nseg = 0;                              // ring entries of earlier segments
+    uint32_t pc[2] = {0, 0};
+    bool ok = true;
+    for (long long u = u0; u < u1 && ok; u += seg.n, ++nseg) {
+      seg.at(a, QT, u, u1);
+      if (lane == 0) {
+        const int steps = PAIR ? 2 * seg.n : seg.n;
+        ok = mbar_wait(smem_u32(q_full), nseg & 1, abort);
+        tc_fence_after();
+        auto issue_s = [&](int s) {
+          const int j = PAIR ? s >> 1 : s, p = s & 1;
+          const int c = cnt + 2 * j, st = c % C::STAGES;
+          if ((!PAIR || p == 0) && !mbar_wait(smem_u32(&full[st]), (c / C::STAGES) & 1, abort)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < DH / 16; ++k) {
+            const uint32_t off = (k >> 2) * C::BOX + (k & 3) * 32;
+            tc_mma(tmem + p * 128, desc_sw128(smem_u32(sQ + (PAIR ? p * C::TILE : 0)) + off),
+                   desc_sw128(smem_u32(sKV + st * C::TILE) + off), idS, k > 0);
+          }
+          if (!PAIR || p == 1) tc_commit(smem_u32(&empty[st]));
+          tc_commit(smem_u32(&s_full[p]));
+          return true;
+        };
+        auto issue_pv = [&](int s) {
+          const int j = PAIR ? s >> 1 : s, p = s & 1;
+          const int c = cnt + 2 * j + 1, st = c % C::STAGES;
+          if (!mbar_wait(smem_u32(&p_full[p]), pc[p] & 1, abort)) return false;
+          ++pc[p];
+          if (!mbar_wait(smem_u32(&full[st]), (c / C::STAGES) & 1, abort)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < CT_KB / 16; ++k)
+            tc_mma_ts(tmem + C::O_COL + p * 128, tmem + p * 128 + k * 8,
+                      desc_sw128_mn(smem_u32(sKV + st * C::TILE) + k * 2048, C::BOX), idO,
+                      s >= 2 || k > 0);
+          if (!PAIR || p == 1) tc_commit(smem_u32(&empty[st]));
+          if (s + 2 >= steps) tc_commit(smem_u32(&o_full[p]));
+          return true;
+        };
+        for (int s = 0; ok && s < min(2, steps); ++s) ok = issue_s(s);
+        for (int s = 0; ok && s < steps; ++s) {
+          ok = issue_pv(s);
+          if (ok && s + 2 < steps) ok = issue_s(s + 2);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      cnt += 2 * seg.n;
+      seg.done(a);
+    }
+  } else if (warp >= 4) {
+    // ---------------- softmax: thread = packed row `r` of pair `p`
+    const int p = (warp - 4) >> 2, r = tid & 127;
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tS = tl + p * 128, tO = tl + C::O_COL + p * 128;
+    const int bar = 1 + p;
+    uint32_t sc = 0, oc = 0;                            // phases of s_full and o_full seen
+    int cnt = 0;                                        // ring entries of earlier segments
+    const int np = CT_KB >> a.c.ps_log2;
+    const uint32_t all_pages = (1u << np) - 1u;
+    for (long long u = u0; u < u1; u += seg.n) {
+      seg.at(a, QT, u, u1);
+      const SeenBlocks<CT_KB> blocks(seg.seen);
+      const NewRows nr = new_rows(a.cu, a.kv_len, seg.b, a.T);
+      const int all = min(nr.n, a.max_rows) * a.G;
+      const int xw = seg.x0 + (PAIR ? p * 128 : 0);     // this warpgroup's first packed row
+      const int x = xw + r;
+      const bool live = x < all;
+      const int qi = live ? x / a.G : 0, hq = seg.g * a.G + (live ? x - qi * a.G : 0);
+      const int pq = a.q_pos ? __ldg(a.q_pos + nr.first + qi) : nr.L - nr.n + qi;
+      // ---- Q to shared memory, one row a thread
+      if (PAIR || p == 0) {
+        uint8_t* dst = sQ + (PAIR ? p * C::TILE : 0);
+        const uint4* src = (const uint4*)((const bf16*)a.q + (nr.first + qi) * a.qs + hq * DH);
+#pragma unroll
+        for (int c = 0; c < DH / 8; ++c) {
+          const uint4 v = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          *(uint4*)(dst + (c >> 3) * C::BOX + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      mbar_arrive(smem_u32(q_full));
+      // positions that every row of this warpgroup sees: [.., pmin], window from pmax
+      const int pmin = nr.L - nr.n + min(xw, all - 1) / a.G;
+      const int pmax = nr.L - nr.n + (min(xw + 128, all) - 1) / a.G;
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+      for (int j = PAIR ? 0 : p; j < seg.n; j += PAIR ? 1 : 2) {
+        const int r0 = blocks.row(seg.j0 + j);
+        const int ring = cnt + 2 * j + 1;               // the block's V tile
+        // which of the block's pages exist (loaded before the scores are waited for)
+        uint32_t pages;
+        {
+          const int pr = r0 + (lane << a.c.ps_log2);
+          pages = __ballot_sync(0xffffffffu, lane < np && cache_page(a.c, seg.b, pr) >= 0);
+        }
+        const bool inside = r0 >= seg.seen.lo && r0 + CT_KB <= seg.seen.hi;
+        const bool open = !a.c.pos && inside && pages == all_pages && r0 + CT_KB - 1 <= pmin &&
+                          (a.window == 0 || pmax - r0 < a.window);
+        uint32_t okw[4] = {~0u, ~0u, ~0u, ~0u};         // keys that exist and someone sees
+        if (!open) {
+          const int kr = r0 + r;
+          const bool ok = row_seen(seg.seen, kr) && ((pages >> (r >> a.c.ps_log2)) & 1u);
+          named_sync(bar, 128);                         // the last block's readers are done
+          if (a.c.pos) {
+            int kp = 0;
+            if (ok) kp = a.c.pos[cache_row(a.c, cache_page(a.c, seg.b, kr), seg.g, kr)];
+            s_kpos[p * 128 + r] = kp;
+          }
+          // value rows in pages that exist but that nobody sees may hold
+          // anything: zero them, as 0 x NaN would not be 0
+          if (!inside) {
+            (void)mbar_wait(smem_u32(&full[ring % C::STAGES]), (ring / C::STAGES) & 1, abort);
+            if (!row_seen(seg.seen, kr)) {
+              uint8_t* v = sKV + (ring % C::STAGES) * C::TILE + r * 128;
+#pragma unroll
+              for (int c = 0; c < DH / 8; ++c)
+                *(uint4*)(v + (c >> 3) * C::BOX + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          named_sync(bar, 128);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int c = r0 + k * 32 + lane;
+            okw[k] = __ballot_sync(0xffffffffu, row_seen(seg.seen, c) &&
+                                                    ((pages >> ((k * 32 + lane) >> a.c.ps_log2)) & 1u));
+          }
+        }
+        (void)mbar_wait(smem_u32(&s_full[p]), sc & 1, abort);
+        ++sc;
+        tc_fence_after();
+        uint32_t s[2][64];
+        tmem_ld64(tS, s[0]);
+        tmem_ld64(tS + 64, s[1]);
+        if (!open) {
+#pragma unroll
+          for (int c = 0; c < CT_KB; ++c) {
+            const int pk = a.c.pos ? s_kpos[p * 128 + c] : r0 + c;
+            if (!(((okw[c >> 5] >> (c & 31)) & 1u) && sees(pq, pk, a.window, a.sinks)))
+              s[c >> 6][c & 63] = 0xff800000u;          // -inf
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < CT_KB; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c >> 6][c & 63]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        if (first) {
+          m = top;
+          first = false;
+        } else if (__any_sync(0xffffffffu, top > m + 8.f)) {
+          const float mn = fmaxf(m, top);
+          const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+          m = mn;
+          l *= f;
+#pragma unroll
+          for (int c = 0; c < DH; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(tO + c, o);
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float p0 = ex2(fmaf(__uint_as_float(s[h][c]), a.scale_log2, -ref));
+            const float p1 = ex2(fmaf(__uint_as_float(s[h][c + 1]), a.scale_log2, -ref));
+            ls[c & 2] += p0;
+            ls[(c & 2) + 1] += p1;
+            pk[c >> 1] = pack_bf16x2(p0, p1);
+          }
+          tmem_st32(tS + h * 32, pk);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&p_full[p]));
+      }
+      // ---- the segment's result
+      const bool whole = seg.j0 == 0 && seg.n == seg.nb;
+      const size_t prt = ((size_t)blockIdx.x * 2 + (u == u0 ? 0 : 1)) * QT + (x - seg.x0);
+      const int t = nr.first + qi;
+      bf16* const dst = (bf16*)a.out + t * a.os + hq * DH;
+      auto put = [&](int c0, const uint32_t* o, float f) {   // 32 columns
+        if (!live) return;
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[k] = pack_bf16x2(__uint_as_float(o[i + 2 * k]) * f, __uint_as_float(o[i + 2 * k + 1]) * f);
+            *(uint4*)(dst + c0 + i) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *(uint4*)(a.part + prt * DH + c0 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        }
+      };
+      auto stats = [&](float mm, float ll) {
+        if (!live) return;
+        if (!whole) a.part_ml[prt] = make_float2(mm, ll);
+        else if (a.lse)
+          a.lse[(size_t)t * a.n_heads + hq] =
+              ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+      };
+      if (PAIR || p == 0 || seg.n > 1) (void)mbar_wait(smem_u32(&o_full[p]), oc++ & 1, abort);
+      tc_fence_after();
+      if constexpr (PAIR) {
+        const float f = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int c = 0; c < DH; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c, o);
+          put(c, o, f);
+        }
+        stats(m, l);
+      } else {
+        // pair 1's state goes to pair 0 through the second Q tile: (max, sum),
+        // then half of O at a time, stored [column][row]
+        float* buf = (float*)(sQ + C::TILE);
+        if (p == 1) ((float2*)buf)[r] = make_float2(m, l);
+        named_sync(3, 256);
+        const float2 o1 = ((const float2*)buf)[r];
+        named_sync(3, 256);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (p == 1 && seg.n > 1) {
+#pragma unroll
+            for (int c = 0; c < DH / 2; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + h * (DH / 2) + c, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) buf[(c + i) * 128 + r] = __uint_as_float(o[i]);
+            }
+          }
+          named_sync(3, 256);
+          if (p == 0) {
+            const float mm = fmaxf(m, o1.x), rf = mm == -INFINITY ? 0.f : mm;
+            const float f0 = ex2(m - rf), f1 = seg.n > 1 ? ex2(o1.x - rf) : 0.f;
+            const float ll = l * f0 + (seg.n > 1 ? o1.y * f1 : 0.f);
+            const float f = ll > 0.f ? 1.f / ll : 0.f;
+#pragma unroll
+            for (int c = 0; c < DH / 2; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + h * (DH / 2) + c, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                float v = __uint_as_float(o[i]) * f0;
+                if (seg.n > 1) v = fmaf(buf[(c + i) * 128 + r], f1, v);
+                o[i] = __float_as_uint(v);
+              }
+              put(h * (DH / 2) + c, o, f);
+            }
+            if (h == 0) stats(mm, ll);
+          }
+          named_sync(3, 256);
+        }
+      }
+      tc_fence_before();
+      cnt += 2 * seg.n;
+      seg.done(a);
+    }
+  }
+
+  // ---------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (*abort) {
+    if (tid == 0) atomicExch(a.plan_n + 1, CT_ERR_TIMEOUT);
+    // let copies and MMAs already issued land before the memory goes away
+    const unsigned long long t0 = gtimer();
+    while (gtimer() - t0 < 50000ull) {
+    }
+    __syncthreads();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace fm

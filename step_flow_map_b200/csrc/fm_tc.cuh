@@ -19,7 +19,6 @@
 // an error code, lets in-flight copies land, frees its TMEM and exits.
 #pragma once
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <stdio.h>
 
 #include <type_traits>
@@ -602,25 +601,10 @@ k_tc_gemm(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUte
 }
 
 // ------------------------------------------------------------------ host side
-inline PFN_cuTensorMapEncodeTiled_v12000 tc_encoder(char* err, size_t errlen) {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    cudaDriverEntryPointQueryResult q;
-    void* p = nullptr;
-    cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
-    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !p) {
-      snprintf(err, errlen, "cuTensorMapEncodeTiled unavailable (%s)", cudaGetErrorString(e));
-      return nullptr;
-    }
-    fn = (PFN_cuTensorMapEncodeTiled_v12000)p;
-  }
-  return fn;
-}
-
 // 2-D K-major bf16 map of a [rows][ld] matrix with `Kd` used columns; box 64 x box_rows.
 inline bool tc_encode(CUtensorMap* m, const void* ptr, int Kd, int rows, int ld, int box_rows,
                       char* err, size_t errlen) {
-  auto enc = tc_encoder(err, errlen);
+  auto enc = tma_encoder(err, errlen);
   if (!enc) return false;
   if (((uintptr_t)ptr & 15) || (ld % 8)) {
     snprintf(err, errlen, "tensor map: base %p / leading dim %d not 16-byte aligned", ptr, ld);
