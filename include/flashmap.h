@@ -295,7 +295,7 @@ fm_status fm_verify_greedy_noalloc(const float *target_logits, const int32_t *dr
  *                weight each cached row got so far, or NULL
  *   page_table   device [n_seqs, table_stride] int32; row r of sequence b
  *                lives in page page_table[b][r / page_size].  Entries past a
- *                sequence's rows are not read.  A row whose entry lies
+ *                sequence's rows do not matter.  A row whose entry lies
  *                outside [0, n_pages) does not exist: nothing is written to
  *                it and no query sees it.
  * page_size is 16, 32, 64 or 128; head_dim 64 or 128 (bf16), 32, 64 or 128
@@ -359,8 +359,9 @@ fm_status fm_cache_append(const fm_paged_cache *cache, const fm_append_args *a, 
  *   accumulate   != 0: cache->weight[row] += the probabilities the row gets,
  *                summed over the new rows and the query heads of its head
  *   lse          device [T, n_heads] fp32 log-sum-exp of the scores, or NULL
- * With cache->pos q_pos must be given.  A query that sees nothing gets zeros
- * and lse -inf.  Rows at or past kv_len and rows that no query of the call
+ * With cache->pos q_pos must be given; without it a new row's position is its
+ * cache row, whatever q_pos says.  A query that sees nothing gets zeros and
+ * lse -inf.  Rows at or past kv_len and rows that no query of the call
  * sees may hold anything, NaN included; a non-finite value in a row that some
  * query sees can reach the sequence's other queries.  Running maxima, sums
  * and outputs are fp32; bf16 probabilities enter the value product rounded

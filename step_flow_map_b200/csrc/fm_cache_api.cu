@@ -69,6 +69,8 @@ fm_status check_rows(const fm_paged_cache* c, int T, int B, int n_heads) {
   if (n_heads % c->n_kv_heads)
     return set_err(FM_ERR_ARG, "n_heads %d is not a multiple of n_kv_heads %d", n_heads,
                    c->n_kv_heads);
+  if (n_heads / c->n_kv_heads > 128)
+    return set_err(FM_ERR_UNSUPPORTED, "more than 128 query heads per key/value head");
   return FM_OK;
 }
 
@@ -179,7 +181,7 @@ struct AttnPlan {
   // M), else k_cache_attn_tc, in pairs of 128-row tiles past 128 rows; fp32:
   // k_cache_attn_simt with 16- or 64-row tiles
   enum { DECODE, TC_ONE, TC_PAIR, SIMT } kind = SIMT;
-  int qt = 0, grid = 0;
+  int qt = 0, rt = 0, tile_rows = 0, grid = 0;   // rows of a partial; see CacheAttnArgs
   int64_t tiles = 0;
   size_t o_first = 0, o_tile = 0, o_lse = 0, o_ml = 0, o_part = 0, total = 0;
 };
@@ -203,16 +205,21 @@ fm_status plan_attention(const fm_paged_cache* c, const fm_attention_args* a, At
   FM_TRY(device_sms(&sms));
   const int64_t G = a->n_heads / c->n_kv_heads;
   const int64_t rows = a->max_rows * G;
-  p->qt = rows <= 16 ? 16 : 64;
+  p->qt = p->rt = p->tile_rows = rows <= 16 ? 16 : 64;
   p->grid = 2 * sms;
   if (c->dtype == FM_BF16) {
-    p->kind = rows <= 16 ? AttnPlan::DECODE : rows <= 128 ? AttnPlan::TC_ONE : AttnPlan::TC_PAIR;
+    p->kind = AttnPlan::DECODE;
     if (rows > 16) {
-      p->qt = rows <= 128 ? 128 : 256;
+      // whole queries per 128-row tile, so that one TMA box brings them
+      p->rt = (int)(128 / G * G);
+      const bool pair = rows > p->rt;
+      p->kind = pair ? AttnPlan::TC_PAIR : AttnPlan::TC_ONE;
+      p->qt = pair ? 256 : 128;
+      p->tile_rows = pair ? 2 * p->rt : p->rt;
       p->grid = sms;
     }
   }
-  p->tiles = ((int64_t)a->T * G) / p->qt + a->B;
+  p->tiles = ((int64_t)a->T * G) / p->tile_rows + a->B;
   size_t at = 256;
   p->o_first = at;
   at = up256(at + (size_t)(p->tiles + 1) * sizeof(long long));
@@ -233,7 +240,7 @@ fm_status launch_simt(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_
   using C = fm::CsCfg<DH, QT>;
   FM_CUDA(fm::set_smem_once(fm::k_cache_attn_simt<T, DH, QT>, C::SMEM));
   FM_LAUNCH_OK("cache attention plan",
-               fm::launch_pdl(fm::k_cache_plan<QT, fm::CS_KB>, dim3(1), dim3(fm::CP_THREADS), 0, st, k));
+               fm::launch_pdl(fm::k_cache_plan<fm::CS_KB>, dim3(1), dim3(fm::CP_THREADS), 0, st, k));
   FM_LAUNCH_OK("cache attention", fm::launch_pdl(fm::k_cache_attn_simt<T, DH, QT>, dim3(p.grid),
                                                  dim3(fm::CS_THREADS), C::SMEM, st, k));
   FM_LAUNCH_OK("cache attention join",
@@ -281,11 +288,24 @@ fm_status launch_tc(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_t 
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return set_err(FM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   }
+  // the queries as [T][key/value heads][G][DH]; a box is 64 columns of the G
+  // heads of rt / G rows
+  CUtensorMap mq;
+  {
+    const cuuint64_t d[4] = {(cuuint64_t)DH, (cuuint64_t)k.G, (cuuint64_t)k.c.n_kv, (cuuint64_t)k.T};
+    const cuuint64_t st4[3] = {(cuuint64_t)DH * 2, (cuuint64_t)DH * 2 * k.G, (cuuint64_t)std::max<int64_t>(k.qs, (int64_t)k.n_heads * DH) * 2};
+    const cuuint32_t b4[4] = {64, (cuuint32_t)k.G, 1, (cuuint32_t)(k.rt / k.G)};
+    const cuuint32_t e4[4] = {1, 1, 1, 1};
+    const CUresult r = enc(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(k.q), d, st4, b4,
+                           e4, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return set_err(FM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  }
   FM_CUDA(fm::set_smem_once(kernel, C::SMEM));
   FM_LAUNCH_OK("cache attention plan",
-               fm::launch_pdl(fm::k_cache_plan<QT, fm::CT_KB>, dim3(1), dim3(fm::CP_THREADS), 0, st, k));
+               fm::launch_pdl(fm::k_cache_plan<fm::CT_KB>, dim3(1), dim3(fm::CP_THREADS), 0, st, k));
   FM_LAUNCH_OK("cache attention", fm::launch_pdl(kernel, dim3(p.grid), dim3(fm::CT_THREADS), C::SMEM,
-                                                 st, mk, mv, k));
+                                                 st, mk, mv, mq, k));
   FM_LAUNCH_OK("cache attention join",
                fm::launch_pdl(fm::k_cache_join<bf16, DH, QT>, dim3(p.grid - 1, QT / 4),
                               dim3(fm::CJ_THREADS), 0, st, k, p.grid));
@@ -346,12 +366,14 @@ extern "C" fm_status fm_cache_attention(const fm_paged_cache* c, const fm_attent
   k.G = a->n_heads / c->n_kv_heads;
   k.max_rows = a->max_rows;
   k.max_kv = a->max_kv;
+  k.rt = p.rt;
+  k.tile_rows = p.tile_rows;
   k.q = a->q;
   k.qs = a->q_stride;
   k.os = a->out_stride;
   k.cu = a->cu_rows;
   k.kv_len = a->kv_len;
-  k.q_pos = a->q_pos;
+  k.q_pos = c->pos ? a->q_pos : nullptr;
   k.scale_log2 = a->scale * 1.4426950408889634f;
   k.window = a->window;
   k.sinks = a->sinks;

@@ -22,6 +22,7 @@ namespace fm {
 struct CacheAttnArgs {
   CacheView c;
   int T, B, n_heads, G, max_rows, max_kv;
+  int rt, tile_rows;               // packed rows of a (half) tile that are used; of a tile
   const void* q;
   int64_t qs, os;
   const int *cu, *kv_len, *q_pos;
@@ -32,7 +33,8 @@ struct CacheAttnArgs {
   // workspace
   int* plan_n;                     // [0]: number of tiles, [1]: status of the call
   long long* plan_first;           // [tiles + 1]: first unit of each tile, heads apart
-  int4* plan_tile;                 // [tiles][2]: (b, tile, -, -), (s_end, lo, hi, -)
+  int4* plan_tile;                 // [tiles][2]: (b, first packed row, first new row, packed rows
+                                   //   of the sequence), (s_end, lo, hi, position of new row 0)
   float* part;                     // [grid][2][QT][DH]
   float2* part_ml;                 // [grid][2][QT]: (max, sum), log2 units
 };
@@ -81,11 +83,12 @@ __device__ __forceinline__ bool sees(int pq, int pk, int window, int sinks) {
 // ------------------------------------------------------------------ plan
 // One CTA lists the tiles of every sequence and prefix-sums their blocks.
 constexpr int CP_THREADS = 1024;
-template <int QT, int KB>
+template <int KB>
 __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a) {
   __shared__ int s_tiles[257];
   __shared__ long long s_warp[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int QT = a.tile_rows;
   pdl_wait();
   pdl_trigger();
   if (tid < 256) {
@@ -116,8 +119,8 @@ __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a
       const int rows = min(s.n, a.max_rows) * a.G;
       const SeenRows r = seen_rows(a, s, tile * QT / a.G, (min(rows, (tile + 1) * QT) - 1) / a.G);
       nb = SeenBlocks<KB>(r).nb;
-      a.plan_tile[2 * e] = make_int4(b, tile, 0, 0);
-      a.plan_tile[2 * e + 1] = make_int4(r.s_end, r.lo, r.hi, 0);
+      a.plan_tile[2 * e] = make_int4(b, tile * QT, s.first, rows);
+      a.plan_tile[2 * e + 1] = make_int4(r.s_end, r.lo, r.hi, s.L - s.n);
     }
     long long x = nb;
 #pragma unroll
@@ -220,15 +223,14 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
     const int b = pt.x;
     const SeenRows seen = {ps.x, ps.y, ps.z};
     const SeenBlocks<CS_KB> blocks(seen);
-    const NewRows s = new_rows(a.cu, a.kv_len, b, a.T);
-    const int x0 = pt.y * QT, rows = min(QT, min(s.n, a.max_rows) * a.G - x0);
+    const int x0 = pt.y, row0 = pt.z, rows = min(QT, pt.w - x0);
     __syncthreads();
     for (int i = tid; i < QT * (DH / VE); i += CS_THREADS) {
       const int r = i / (DH / VE), c = (i % (DH / VE)) * VE;
       float f[VE];
       if (r < rows) {
         const int x = x0 + r;
-        Vec16<T>::unpack(*(const uint4*)((const T*)a.q + (s.first + x / a.G) * a.qs +
+        Vec16<T>::unpack(*(const uint4*)((const T*)a.q + (row0 + x / a.G) * a.qs +
                                          (g * a.G + x % a.G) * DH + c), f);
       } else {
 #pragma unroll
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
     for (int i = 0; i < C::RPT; ++i) {
       const int r = tr + C::TR * i;
       const int qi = (x0 + (r < rows ? r : 0)) / a.G;
-      pq[i] = a.q_pos ? __ldg(a.q_pos + s.first + qi) : s.L - s.n + qi;
+      pq[i] = a.q_pos ? __ldg(a.q_pos + row0 + qi) : ps.w + qi;
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
       const int r = tr + C::TR * i;
       if (r >= rows) continue;
       if (whole) {
-        const int x = x0 + r, t = s.first + x / a.G, h = g * a.G + x % a.G;
+        const int x = x0 + r, t = row0 + x / a.G, h = g * a.G + x % a.G;
         const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
         T* dst = (T*)a.out + t * a.os + h * DH;
 #pragma unroll
@@ -422,12 +424,12 @@ __global__ void __launch_bounds__(CJ_THREADS) k_cache_join(const CacheAttnArgs a
   if (first == u || w.start(c - 1) > first) return;
   const int last = w.cta_of(first + nb - 1);
   const int4 pt = a.plan_tile[2 * e];
-  const NewRows s = new_rows(a.cu, a.kv_len, pt.x, a.T);
   const int r = blockIdx.y * (CJ_THREADS / 32) + (threadIdx.x >> 5);
-  const int x = pt.y * QT + r;
-  if (r >= QT || x >= min(s.n, a.max_rows) * a.G) return;
+  // partial row r: row r % 128 of half tile r / 128
+  const int x = pt.y + (r >> 7) * a.rt + (r & 127);
+  if (r >= QT || (r & 127) >= a.rt || x >= pt.w) return;
   // run c - 1 began the tile
-  join_row<T, DH>(a, c - 1, last, w.start(c - 1) == first ? 0 : 1, QT, r, s.first + x / a.G,
+  join_row<T, DH>(a, c - 1, last, w.start(c - 1) == first ? 0 : 1, QT, r, pt.z + x / a.G,
                   g * a.G + x % a.G);
 }
 

@@ -2,7 +2,7 @@
 // rows per key/value head: drafted blocks, prompts) on tcgen05.
 //
 // Per block of 128 cache rows: S = Q K^T (128 packed rows x 128 keys, fp32 in
-// TMEM), P = 2^(S - m) rounded to bf16 over S's own columns, O += P V with P
+// TMEM), P = 2^(S - m) rounded to bf16 over the second half of S, O += P V with P
 // read from TMEM.  Keys and values come page by page through TMA into a ring
 // of 128-row tiles (128-byte swizzle): K as the K-major operand, V as it lies,
 // MN-major.  Two softmax warpgroups, one thread per packed row, work on two
@@ -37,24 +37,29 @@ struct CtCfg {
   static constexpr int BOX = 128 * 128;                // its 64-column half
   static constexpr int STAGES = DH == 128 ? 5 : 8;
   static constexpr int O_COL = 256;                    // TMEM: S0, S1 (128 each), O0, O1
-  static constexpr int BARS = 2 * STAGES + 7;          // full, empty, s_full, p_full, o_full, q_full
+  static constexpr int P_COL = 64;                     // P over the second half of its S
+  static constexpr int BARS = 2 * STAGES + 12;         // full, empty; per pair s_full, p_half,
+                                                       //   p_full, o_full, q_full, q_empty
   static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + 2 * 128 * 4 + 256;
 };
 
 // A stretch of one tile's blocks inside a CTA's run.
 struct TileSeg {
-  int e, g, j0, n, nb, b, x0;
-  SeenRows seen;
-  __device__ __forceinline__ void at(const CacheAttnArgs& a, int qt, long long u, long long u1) {
+  int e, g, j0, n, nb, b, x0, row0, all, p0;   // row0: first new row; all: its packed rows; p0:
+  SeenRows seen;                               //   position of its first new row
+  __device__ __forceinline__ void at(const CacheAttnArgs& a, long long u, long long u1) {
     const long long t0 = a.plan_first[e];
     nb = (int)(a.plan_first[e + 1] - t0);
-    const long long d = u - t0 * a.c.n_kv;
-    g = (int)(d / nb);
-    j0 = (int)(d - (long long)g * nb);
+    const unsigned d = (unsigned)(u - t0 * a.c.n_kv);   // < blocks x heads of one tile
+    g = (int)(d / (unsigned)nb);
+    j0 = (int)(d - (unsigned)g * (unsigned)nb);
     n = (int)min((long long)(nb - j0), u1 - u);
     const int4 t = a.plan_tile[2 * e], s = a.plan_tile[2 * e + 1];
     b = t.x;
-    x0 = t.y * qt;
+    x0 = t.y;
+    row0 = t.z;
+    all = t.w;
+    p0 = s.w;
     seen.s_end = s.x;
     seen.lo = s.y;
     seen.hi = s.z;
@@ -64,12 +69,17 @@ struct TileSeg {
   }
 };
 
+// Bits 0 .. n - 1 of a word, for any n.
+__device__ __forceinline__ unsigned long long below(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
 template <int DH, bool PAIR>
 __global__ void __launch_bounds__(CT_THREADS, 1)
 k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-                const CacheAttnArgs a) {
+                const __grid_constant__ CUtensorMap mapQ, const CacheAttnArgs a) {
   using C = CtCfg<DH>;
-  constexpr int QT = PAIR ? 256 : 128;
+  constexpr int QT = PAIR ? 256 : 128;                 // partial rows of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sQ = base;                                  // two tiles; the second is the merge
@@ -77,7 +87,8 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
   int* s_kpos = (int*)(sKV + C::STAGES * C::TILE);     // [2][128] key positions
   uint64_t* bars = (uint64_t*)(s_kpos + 256);
   uint64_t *full = bars, *empty = bars + C::STAGES, *s_full = empty + C::STAGES,
-           *p_full = s_full + 2, *o_full = p_full + 2, *q_full = o_full + 2;
+           *p_half = s_full + 2, *p_full = p_half + 2, *o_full = p_full + 2, *q_full = o_full + 2,
+           *q_empty = q_full + 2;
   uint32_t* tmem_slot = (uint32_t*)(bars + C::BARS);
   volatile int* abort = (volatile int*)(tmem_slot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -90,9 +101,11 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&p_full[i]), 128);
+      mbar_init(smem_u32(&p_half[i]), 128);
       mbar_init(smem_u32(&o_full[i]), 1);
+      mbar_init(smem_u32(&q_full[i]), 1);
+      mbar_init(smem_u32(&q_empty[i]), PAIR ? 128 : 256);
     }
-    mbar_init(smem_u32(q_full), 256);
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -118,10 +131,24 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     // ---------------- TMA producer: lane i takes the block's i-th page
     const int np = CT_KB >> a.c.ps_log2, ps = 1 << a.c.ps_log2;
     const int gone = a.c.n_pages * a.c.n_kv * ps;      // past the last row: reads zeros
-    int cnt = 0;
+    int cnt = 0, nseg = 0;
     bool go = true;                                    // the same in every lane
-    for (long long u = u0; u < u1 && go; u += seg.n) {
-      seg.at(a, QT, u, u1);
+    for (long long u = u0; u < u1 && go; u += seg.n, ++nseg) {
+      seg.at(a, u, u1);
+      // the tile's queries: G heads of a.rt / G rows, in packed order
+      if (lane == 0) {
+#pragma unroll
+        for (int p = 0; p < (PAIR ? 2 : 1) && go; ++p) {
+          go = mbar_wait(smem_u32(&q_empty[p]), (nseg & 1) ^ 1, abort);
+          if (!go) break;
+          mbar_expect_tx(smem_u32(&q_full[p]), a.rt * DH * 2);
+#pragma unroll
+          for (int h = 0; h < DH / 64; ++h)
+            tma_load_4d(smem_u32(sQ + p * C::TILE + h * C::BOX), &mapQ, h * 64, 0, seg.g,
+                        seg.row0 + (seg.x0 + p * a.rt) / a.G, smem_u32(&q_full[p]));
+        }
+      }
+      go = __shfl_sync(0xffffffffu, go, 0);
       const SeenBlocks<CT_KB> blocks(seg.seen);
       for (int j = 0; j < seg.n && go; ++j) {
         const int r = blocks.row(seg.j0 + j) + lane * ps;
@@ -159,14 +186,13 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     uint32_t pc[2] = {0, 0};
     bool ok = true;
     for (long long u = u0; u < u1 && ok; u += seg.n, ++nseg) {
-      seg.at(a, QT, u, u1);
+      seg.at(a, u, u1);
       if (lane == 0) {
         const int steps = PAIR ? 2 * seg.n : seg.n;
-        ok = mbar_wait(smem_u32(q_full), nseg & 1, abort);
-        tc_fence_after();
         auto issue_s = [&](int s) {
           const int j = PAIR ? s >> 1 : s, p = s & 1;
           const int c = cnt + 2 * j, st = c % C::STAGES;
+          if (s < (PAIR ? 2 : 1) && !mbar_wait(smem_u32(&q_full[p]), nseg & 1, abort)) return false;
           if ((!PAIR || p == 0) && !mbar_wait(smem_u32(&full[st]), (c / C::STAGES) & 1, abort)) return false;
           tc_fence_after();
 #pragma unroll
@@ -182,15 +208,19 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         auto issue_pv = [&](int s) {
           const int j = PAIR ? s >> 1 : s, p = s & 1;
           const int c = cnt + 2 * j + 1, st = c % C::STAGES;
-          if (!mbar_wait(smem_u32(&p_full[p]), pc[p] & 1, abort)) return false;
-          ++pc[p];
           if (!mbar_wait(smem_u32(&full[st]), (c / C::STAGES) & 1, abort)) return false;
-          tc_fence_after();
+          // the block's second 64 keys are ready first
 #pragma unroll
-          for (int k = 0; k < CT_KB / 16; ++k)
-            tc_mma_ts(tmem + C::O_COL + p * 128, tmem + p * 128 + k * 8,
-                      desc_sw128_mn(smem_u32(sKV + st * C::TILE) + k * 2048, C::BOX), idO,
-                      s >= 2 || k > 0);
+          for (int h = 1; h >= 0; --h) {
+            if (!mbar_wait(smem_u32(h ? &p_half[p] : &p_full[p]), pc[p] & 1, abort)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int k = h * 4; k < h * 4 + 4; ++k)
+              tc_mma_ts(tmem + C::O_COL + p * 128, tmem + p * 128 + C::P_COL + k * 8,
+                        desc_sw128_mn(smem_u32(sKV + st * C::TILE) + k * 2048, C::BOX), idO,
+                        s >= 2 || k != 4);
+          }
+          ++pc[p];
           if (!PAIR || p == 1) tc_commit(smem_u32(&empty[st]));
           if (s + 2 >= steps) tc_commit(smem_u32(&o_full[p]));
           return true;
@@ -216,101 +246,127 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     const int np = CT_KB >> a.c.ps_log2;
     const uint32_t all_pages = (1u << np) - 1u;
     for (long long u = u0; u < u1; u += seg.n) {
-      seg.at(a, QT, u, u1);
+      seg.at(a, u, u1);
       const SeenBlocks<CT_KB> blocks(seg.seen);
-      const NewRows nr = new_rows(a.cu, a.kv_len, seg.b, a.T);
-      const int all = min(nr.n, a.max_rows) * a.G;
-      const int xw = seg.x0 + (PAIR ? p * 128 : 0);     // this warpgroup's first packed row
+      const int all = seg.all;
+      const int xw = seg.x0 + (PAIR ? p * a.rt : 0);    // this warpgroup's first packed row
       const int x = xw + r;
-      const bool live = x < all;
+      const bool live = r < a.rt && x < all;
       const int qi = live ? x / a.G : 0, hq = seg.g * a.G + (live ? x - qi * a.G : 0);
-      const int pq = a.q_pos ? __ldg(a.q_pos + nr.first + qi) : nr.L - nr.n + qi;
-      // ---- Q to shared memory, one row a thread
-      if (PAIR || p == 0) {
-        uint8_t* dst = sQ + (PAIR ? p * C::TILE : 0);
-        const uint4* src = (const uint4*)((const bf16*)a.q + (nr.first + qi) * a.qs + hq * DH);
-#pragma unroll
-        for (int c = 0; c < DH / 8; ++c) {
-          const uint4 v = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-          *(uint4*)(dst + (c >> 3) * C::BOX + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      }
-      mbar_arrive(smem_u32(q_full));
+      const int pq = a.q_pos ? __ldg(a.q_pos + seg.row0 + qi) : seg.p0 + qi;
       // positions that every row of this warpgroup sees: [.., pmin], window from pmax
-      const int pmin = nr.L - nr.n + min(xw, all - 1) / a.G;
-      const int pmax = nr.L - nr.n + (min(xw + 128, all) - 1) / a.G;
+      const int pmin = seg.p0 + min(xw, all - 1) / a.G;
+      const int pmax = seg.p0 + (min(xw + a.rt, all) - 1) / a.G;
       float m = -INFINITY, l = 0.f;
       bool first = true;
+      // lane's page-table entry of a block, loaded one block before it is looked at
+      auto page_of = [&](int j) {
+        const int i = (blocks.row(seg.j0 + j) >> a.c.ps_log2) + lane;
+        return lane < np && j < seg.n && i < a.c.table_stride
+                   ? __ldg(a.c.table + (size_t)seg.b * a.c.table_stride + i) : -1;
+      };
+      int page = page_of(PAIR ? 0 : p);
       for (int j = PAIR ? 0 : p; j < seg.n; j += PAIR ? 1 : 2) {
         const int r0 = blocks.row(seg.j0 + j);
         const int ring = cnt + 2 * j + 1;               // the block's V tile
-        // which of the block's pages exist (loaded before the scores are waited for)
-        uint32_t pages;
-        {
-          const int pr = r0 + (lane << a.c.ps_log2);
-          pages = __ballot_sync(0xffffffffu, lane < np && cache_page(a.c, seg.b, pr) >= 0);
-        }
+        const uint32_t pages = __ballot_sync(0xffffffffu, (unsigned)page < (unsigned)a.c.n_pages);
+        page = page_of(j + (PAIR ? 1 : 2));
         const bool inside = r0 >= seg.seen.lo && r0 + CT_KB <= seg.seen.hi;
         const bool open = !a.c.pos && inside && pages == all_pages && r0 + CT_KB - 1 <= pmin &&
                           (a.window == 0 || pmax - r0 < a.window);
-        uint32_t okw[4] = {~0u, ~0u, ~0u, ~0u};         // keys that exist and someone sees
+        unsigned long long see0 = ~0ull, see1 = ~0ull;  // this row's mask of the 128 keys
         if (!open) {
           const int kr = r0 + r;
-          const bool ok = row_seen(seg.seen, kr) && ((pages >> (r >> a.c.ps_log2)) & 1u);
-          named_sync(bar, 128);                         // the last block's readers are done
-          if (a.c.pos) {
-            int kp = 0;
-            if (ok) kp = a.c.pos[cache_row(a.c, cache_page(a.c, seg.b, kr), seg.g, kr)];
-            s_kpos[p * 128 + r] = kp;
-          }
-          // value rows in pages that exist but that nobody sees may hold
-          // anything: zero them, as 0 x NaN would not be 0
-          if (!inside) {
-            (void)mbar_wait(smem_u32(&full[ring % C::STAGES]), (ring / C::STAGES) & 1, abort);
-            if (!row_seen(seg.seen, kr)) {
-              uint8_t* v = sKV + (ring % C::STAGES) * C::TILE + r * 128;
-#pragma unroll
-              for (int c = 0; c < DH / 8; ++c)
-                *(uint4*)(v + (c >> 3) * C::BOX + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          if (!inside || a.c.pos) {
+            named_sync(bar, 128);                       // the last block's readers are done
+            if (a.c.pos) {
+              int kp = 0;
+              if (row_seen(seg.seen, kr) && ((pages >> (r >> a.c.ps_log2)) & 1u))
+                kp = a.c.pos[cache_row(a.c, cache_page(a.c, seg.b, kr), seg.g, kr)];
+              s_kpos[p * 128 + r] = kp;
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          }
-          named_sync(bar, 128);
+            // value rows in pages that exist but that nobody sees may hold
+            // anything: zero them, as 0 x NaN would not be 0
+            if (!inside) {
+              (void)mbar_wait(smem_u32(&full[ring % C::STAGES]), (ring / C::STAGES) & 1, abort);
+              if (!row_seen(seg.seen, kr)) {
+                uint8_t* v = sKV + (ring % C::STAGES) * C::TILE + r * 128;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int c = r0 + k * 32 + lane;
-            okw[k] = __ballot_sync(0xffffffffu, row_seen(seg.seen, c) &&
-                                                    ((pages >> ((k * 32 + lane) >> a.c.ps_log2)) & 1u));
+                for (int c = 0; c < DH / 8; ++c)
+                  *(uint4*)(v + (c >> 3) * C::BOX + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            named_sync(bar, 128);
+          }
+          // without stored positions a row sees keys [0, c_sink) and [c_lo, c_hi)
+          // of the block (counted from r0; r0 and the ends are cache rows, and
+          // pq + 1 only matters up to hi)
+          const int c_hi = min(seg.seen.hi, min(pq, seg.seen.hi) + 1) - r0;
+          const int c_lo = a.window > 0 && pq >= a.window ? pq - a.window + 1 - r0 : 0;
+          const int c_sink = a.window > 0 ? min(a.sinks - r0, c_hi) : 0;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const int c0 = h * 64, c = c0 + lane;
+            const uint32_t k0 = __ballot_sync(
+                0xffffffffu, row_seen(seg.seen, r0 + c) && ((pages >> (c >> a.c.ps_log2)) & 1u));
+            const uint32_t k1 = __ballot_sync(
+                0xffffffffu,
+                row_seen(seg.seen, r0 + c + 32) && ((pages >> ((c + 32) >> a.c.ps_log2)) & 1u));
+            unsigned long long mine = 0ull;
+            if (a.c.pos) {
+#pragma unroll 4
+              for (int i = 0; i < 64; ++i)
+                mine |= (unsigned long long)sees(pq, s_kpos[p * 128 + c0 + i], a.window, a.sinks) << i;
+            } else {
+              mine = (below(c_hi - c0) & ~below(c_lo - c0)) | below(c_sink - c0);
+            }
+            mine &= (unsigned long long)k1 << 32 | k0;
+            if (h == 0) see0 = mine;
+            else see1 = mine;
           }
         }
         (void)mbar_wait(smem_u32(&s_full[p]), sc & 1, abort);
         ++sc;
+        // the tile's last scores are there: its queries may be replaced
+        if (j + (PAIR ? 1 : 2) >= seg.n) mbar_arrive(smem_u32(&q_empty[PAIR ? p : 0]));
         tc_fence_after();
-        uint32_t s[2][64];
-        tmem_ld64(tS, s[0]);
-        tmem_ld64(tS + 64, s[1]);
-        if (!open) {
+        // 64 scores in registers at a time, first for the maximum, then again
+        // for the exponentials.  (The loops stay rolled: straight-line code of
+        // the whole block no longer fits the instruction caches, and a tile's
+        // prologue and epilogue then run at the speed of their misses.)
+        uint32_t s[64];
+        auto scores = [&](int h) {
+          tmem_ld64(tS + h * 64, s);
+          if (!open) {
+            const unsigned long long see = h ? see1 : see0;
+            const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
 #pragma unroll
-          for (int c = 0; c < CT_KB; ++c) {
-            const int pk = a.c.pos ? s_kpos[p * 128 + c] : r0 + c;
-            if (!(((okw[c >> 5] >> (c & 31)) & 1u) && sees(pq, pk, a.window, a.sinks)))
-              s[c >> 6][c & 63] = 0xff800000u;          // -inf
+            for (int c = 0; c < 64; ++c)
+              if (!(((c < 32 ? lo : hi) >> (c & 31)) & 1u)) s[c] = 0xff800000u;   // -inf
           }
-        }
+        };
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          scores(h);
 #pragma unroll
-        for (int c = 0; c < CT_KB; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c >> 6][c & 63]));
+          for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+        }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        const bool grow = !first && __any_sync(0xffffffffu, top > m + 8.f);
+        float f = 1.f;
         if (first) {
           m = top;
-          first = false;
-        } else if (__any_sync(0xffffffffu, top > m + 8.f)) {
+        } else if (grow) {
           const float mn = fmaxf(m, top);
-          const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+          if (mn != -INFINITY) f = ex2(m - mn);
           m = mn;
           l *= f;
-#pragma unroll
+        }
+        first = false;
+        if (grow) {
+#pragma unroll 1
           for (int c = 0; c < DH; c += 32) {
             uint32_t o[32];
             tmem_ld32(tO + c, o);
@@ -321,39 +377,41 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         }
         const float ref = m == -INFINITY ? 0.f : m;
         float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+        for (int h = 1; h >= 0; --h) {
+          scores(h);
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(s[h][c]), a.scale_log2, -ref));
-            const float p1 = ex2(fmaf(__uint_as_float(s[h][c + 1]), a.scale_log2, -ref));
+            const float p0 = ex2(fmaf(__uint_as_float(s[c]), a.scale_log2, -ref));
+            const float p1 = ex2(fmaf(__uint_as_float(s[c + 1]), a.scale_log2, -ref));
             ls[c & 2] += p0;
             ls[(c & 2) + 1] += p1;
             pk[c >> 1] = pack_bf16x2(p0, p1);
           }
-          tmem_st32(tS + h * 32, pk);
+          tmem_st32(tS + C::P_COL + h * 32, pk);         // over the second half of S
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(smem_u32(h ? &p_half[p] : &p_full[p]));
         }
         l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(smem_u32(&p_full[p]));
       }
-      // ---- the segment's result
+      if (!PAIR && p >= seg.n) mbar_arrive(smem_u32(&q_empty[0]));   // it had no block
+      // ---- the segment's result, one row a thread
       const bool whole = seg.j0 == 0 && seg.n == seg.nb;
-      const size_t prt = ((size_t)blockIdx.x * 2 + (u == u0 ? 0 : 1)) * QT + (x - seg.x0);
-      const int t = nr.first + qi;
-      bf16* const dst = (bf16*)a.out + t * a.os + hq * DH;
+      const size_t prt = ((size_t)blockIdx.x * 2 + (u == u0 ? 0 : 1)) * QT + (PAIR ? p * 128 : 0) + r;
+      const int t = seg.row0 + qi;
       auto put = [&](int c0, const uint32_t* o, float f) {   // 32 columns
         if (!live) return;
         if (whole) {
+          bf16* const dst = (bf16*)a.out + t * a.os + hq * DH + c0;
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
             uint32_t v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               v[k] = pack_bf16x2(__uint_as_float(o[i + 2 * k]) * f, __uint_as_float(o[i + 2 * k + 1]) * f);
-            *(uint4*)(dst + c0 + i) = make_uint4(v[0], v[1], v[2], v[3]);
+            *(uint4*)(dst + i) = make_uint4(v[0], v[1], v[2], v[3]);
           }
         } else {
 #pragma unroll
@@ -372,7 +430,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
       tc_fence_after();
       if constexpr (PAIR) {
         const float f = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < DH; c += 32) {
           uint32_t o[32];
           tmem_ld32(tO + c, o);
@@ -387,10 +445,10 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         named_sync(3, 256);
         const float2 o1 = ((const float2*)buf)[r];
         named_sync(3, 256);
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           if (p == 1 && seg.n > 1) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DH / 2; c += 32) {
               uint32_t o[32];
               tmem_ld32(tO + h * (DH / 2) + c, o);
@@ -404,7 +462,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             const float f0 = ex2(m - rf), f1 = seg.n > 1 ? ex2(o1.x - rf) : 0.f;
             const float ll = l * f0 + (seg.n > 1 ? o1.y * f1 : 0.f);
             const float f = ll > 0.f ? 1.f / ll : 0.f;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DH / 2; c += 32) {
               uint32_t o[32];
               tmem_ld32(tO + h * (DH / 2) + c, o);
