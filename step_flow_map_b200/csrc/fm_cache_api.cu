@@ -181,7 +181,7 @@ struct AttnPlan {
   // M), else k_cache_attn_tc, in pairs of 128-row tiles past 128 rows; fp32:
   // k_cache_attn_simt with 16- or 64-row tiles
   enum { DECODE, TC_ONE, TC_PAIR, SIMT } kind = SIMT;
-  int qt = 0, rt = 0, tile_rows = 0, grid = 0;   // rows of a partial; see CacheAttnArgs
+  int qt = 0, rt = 0, tile_rows = 0, ov = 0, grid = 0;   // rows of a partial; see CacheAttnArgs
   int64_t tiles = 0;
   size_t o_first = 0, o_tile = 0, o_lse = 0, o_ml = 0, o_part = 0, total = 0;
 };
@@ -216,6 +216,7 @@ fm_status plan_attention(const fm_paged_cache* c, const fm_attention_args* a, At
       p->kind = pair ? AttnPlan::TC_PAIR : AttnPlan::TC_ONE;
       p->qt = pair ? 256 : 128;
       p->tile_rows = pair ? 2 * p->rt : p->rt;
+      p->ov = 2;
       p->grid = sms;
     }
   }
@@ -307,7 +308,7 @@ fm_status launch_tc(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_t 
   FM_LAUNCH_OK("cache attention", fm::launch_pdl(kernel, dim3(p.grid), dim3(fm::CT_THREADS), C::SMEM,
                                                  st, mk, mv, mq, k));
   FM_LAUNCH_OK("cache attention join",
-               fm::launch_pdl(fm::k_cache_join<bf16, DH, QT>, dim3(p.grid - 1, QT / 4),
+               fm::launch_pdl(fm::k_cache_join<bf16, DH, QT>, dim3(p.grid - 1, QT / 32),
                               dim3(fm::CJ_THREADS), 0, st, k, p.grid));
   return FM_OK;
 }
@@ -368,6 +369,7 @@ extern "C" fm_status fm_cache_attention(const fm_paged_cache* c, const fm_attent
   k.max_kv = a->max_kv;
   k.rt = p.rt;
   k.tile_rows = p.tile_rows;
+  k.ov = p.ov;
   k.q = a->q;
   k.qs = a->q_stride;
   k.os = a->out_stride;

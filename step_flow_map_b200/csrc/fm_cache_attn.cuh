@@ -23,6 +23,7 @@ struct CacheAttnArgs {
   CacheView c;
   int T, B, n_heads, G, max_rows, max_kv;
   int rt, tile_rows;               // packed rows of a (half) tile that are used; of a tile
+  int ov;                          // units a tile's start and end cost beyond its blocks
   const void* q;
   int64_t qs, os;
   const int *cu, *kv_len, *q_pos;
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a
   long long base = 0;
   for (int e0 = 0; e0 < E; e0 += CP_THREADS) {
     const int e = e0 + tid;
-    long long nb = 0;
+    long long nb = 0;                // units: the blocks, and the tile's overhead
     if (e < E) {
       int b = 0;                   // largest b with s_tiles[b] <= e
       for (int step = 128; step > 0; step >>= 1)
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a
       const NewRows s = new_rows(a.cu, a.kv_len, b, a.T);
       const int rows = min(s.n, a.max_rows) * a.G;
       const SeenRows r = seen_rows(a, s, tile * QT / a.G, (min(rows, (tile + 1) * QT) - 1) / a.G);
-      nb = SeenBlocks<KB>(r).nb;
+      nb = SeenBlocks<KB>(r).nb + a.ov;
       a.plan_tile[2 * e] = make_int4(b, tile * QT, s.first, rows);
       a.plan_tile[2 * e + 1] = make_int4(r.s_end, r.lo, r.hi, s.L - s.n);
     }
@@ -147,7 +148,8 @@ __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a
 }
 
 // The run of units of CTA c of `grid`, and the tile a unit falls in.  Units of
-// a tile: all blocks of head 0, then of head 1, and so on.
+// a tile: for head 0 `ov` units that stand for its start and end and then its
+// blocks, then the same for head 1, and so on.
 struct WorkRun {
   long long N;
   int g;                           // CTAs that have work
@@ -421,16 +423,50 @@ __global__ void __launch_bounds__(CJ_THREADS) k_cache_join(const CacheAttnArgs a
   const int nb = (int)(a.plan_first[e + 1] - t0);
   const int g = (int)((u - t0 * a.c.n_kv) / nb);
   const long long first = t0 * a.c.n_kv + (long long)g * nb;
-  if (first == u || w.start(c - 1) > first) return;
+  // no block lies before u, or an earlier boundary already split the tile
+  if (u <= first + a.ov || w.start(c - 1) > first + a.ov) return;
   const int last = w.cta_of(first + nb - 1);
+  const int slot0 = w.start(c - 1) >= first ? 0 : 1;   // did run c - 1 begin with the tile?
   const int4 pt = a.plan_tile[2 * e];
-  const int r = blockIdx.y * (CJ_THREADS / 32) + (threadIdx.x >> 5);
-  // partial row r: row r % 128 of half tile r / 128
-  const int x = pt.y + (r >> 7) * a.rt + (r & 127);
-  if (r >= QT || (r & 127) >= a.rt || x >= pt.w) return;
-  // run c - 1 began the tile
-  join_row<T, DH>(a, c - 1, last, w.start(c - 1) == first ? 0 : 1, QT, r, pt.z + x / a.G,
-                  g * a.G + x % a.G);
+  if constexpr (QT < 128) {
+    const int r = blockIdx.y * (CJ_THREADS / 32) + (threadIdx.x >> 5), x = pt.y + r;
+    if (r >= QT || x >= pt.w) return;
+    join_row<T, DH>(a, c - 1, last, slot0, QT, r, pt.z + x / a.G, g * a.G + x % a.G);
+  } else {
+    // partials stored [column][row]: a lane per row, a warp per DH / 4 columns;
+    // partial row r is row r % 128 of half tile r / 128
+    constexpr int COLS = DH / (CJ_THREADS / 32);
+    const int r = blockIdx.y * 32 + (threadIdx.x & 31), c0 = (threadIdx.x >> 5) * COLS;
+    const int x = pt.y + (r >> 7) * a.rt + (r & 127);
+    if ((r & 127) >= a.rt || x >= pt.w) return;
+    float m = -INFINITY, l = 0.f, o[COLS];
+    auto slot = [&](int i) { return (size_t)i * 2 + (i == c - 1 ? slot0 : 0); };
+#pragma unroll 4
+    for (int i = c - 1; i <= last; ++i) m = fmaxf(m, a.part_ml[slot(i) * QT + r].x);
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) o[k] = 0.f;
+    for (int i = c - 1; i <= last; ++i) {
+      const float2 ml = a.part_ml[slot(i) * QT + r];
+      const float f = exp2f(ml.x - ref);
+      l = fmaf(ml.y, f, l);
+      const float* p = a.part + (slot(i) * DH + c0) * QT + r;
+#pragma unroll
+      for (int k = 0; k < COLS; ++k) o[k] = fmaf(p[(size_t)k * QT], f, o[k]);
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int t = pt.z + x / a.G, h = g * a.G + x % a.G;
+    T* dst = (T*)a.out + t * a.os + h * DH + c0;
+#pragma unroll
+    for (int k = 0; k < COLS; k += Vec16<T>::N) {
+      float v[Vec16<T>::N];
+#pragma unroll
+      for (int z = 0; z < Vec16<T>::N; ++z) v[z] = o[k + z] * inv;
+      *(uint4*)(dst + k) = Vec16<T>::pack(v);
+    }
+    if (a.lse && c0 == 0)
+      a.lse[(size_t)t * a.n_heads + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
 }
 
 // ------------------------------------------------------------------ weights

@@ -43,18 +43,22 @@ struct CtCfg {
   static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + 2 * 128 * 4 + 256;
 };
 
-// A stretch of one tile's blocks inside a CTA's run.
+// A stretch of one tile's units inside a CTA's run: nv of them, of which the
+// last n are blocks, from block j0 on (see WorkRun; n may be 0).
 struct TileSeg {
-  int e, g, j0, n, nb, b, x0, row0, all, p0;   // row0: first new row; all: its packed rows; p0:
-  SeenRows seen;                               //   position of its first new row
+  int e, g, nv, j0, n, nb, b, x0, row0, all, p0;   // row0: first new row; all: its packed rows;
+  SeenRows seen;                                   //   p0: position of its first new row
   __device__ __forceinline__ void at(const CacheAttnArgs& a, long long u, long long u1) {
     const long long t0 = a.plan_first[e];
-    nb = (int)(a.plan_first[e + 1] - t0);
-    const unsigned d = (unsigned)(u - t0 * a.c.n_kv);   // < blocks x heads of one tile
-    g = (int)(d / (unsigned)nb);
-    j0 = (int)(d - (unsigned)g * (unsigned)nb);
-    n = (int)min((long long)(nb - j0), u1 - u);
+    const int units = (int)(a.plan_first[e + 1] - t0);
     const int4 t = a.plan_tile[2 * e], s = a.plan_tile[2 * e + 1];
+    const unsigned d = (unsigned)(u - t0 * a.c.n_kv);   // < units x heads of one tile
+    g = (int)(d / (unsigned)units);
+    const int v0 = (int)(d - (unsigned)g * (unsigned)units);
+    nv = (int)min((long long)(units - v0), u1 - u);
+    nb = units - a.ov;
+    j0 = max(0, v0 - a.ov);
+    n = max(0, v0 + nv - a.ov) - j0;
     b = t.x;
     x0 = t.y;
     row0 = t.z;
@@ -133,8 +137,9 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     const int gone = a.c.n_pages * a.c.n_kv * ps;      // past the last row: reads zeros
     int cnt = 0, nseg = 0;
     bool go = true;                                    // the same in every lane
-    for (long long u = u0; u < u1 && go; u += seg.n, ++nseg) {
+    for (long long u = u0; u < u1 && go; u += seg.nv) {
       seg.at(a, u, u1);
+      if (seg.n == 0) break;                            // the run ends in a tile's overhead
       // the tile's queries: G heads of a.rt / G rows, in packed order
       if (lane == 0) {
 #pragma unroll
@@ -149,6 +154,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         }
       }
       go = __shfl_sync(0xffffffffu, go, 0);
+      ++nseg;
       const SeenBlocks<CT_KB> blocks(seg.seen);
       for (int j = 0; j < seg.n && go; ++j) {
         const int r = blocks.row(seg.j0 + j) + lane * ps;
@@ -182,57 +188,54 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     // S of a pair is issued after the PV that reads the P it overwrites.
     constexpr uint32_t idS = idesc_bf16<128>();
     constexpr uint32_t idO = idesc_bf16<DH>() | (1u << 16);   // V: MN-major
+    // a wait that gave up is not acted on here: the remaining products run on
+    // whatever is there, every later wait ends at once
+    const uint64_t dk = desc_sw128(smem_u32(sKV)), dq = desc_sw128(smem_u32(sQ)),
+                   dv = desc_sw128_mn(smem_u32(sKV), C::BOX);
     int cnt = 0, nseg = 0;                              // ring entries of earlier segments
-    uint32_t pc[2] = {0, 0};
-    bool ok = true;
-    for (long long u = u0; u < u1 && ok; u += seg.n, ++nseg) {
+    uint32_t pc0 = 0, pc1 = 0;
+    for (long long u = u0; u < u1; u += seg.nv, ++nseg) {
       seg.at(a, u, u1);
-      if (lane == 0) {
-        const int steps = PAIR ? 2 * seg.n : seg.n;
-        auto issue_s = [&](int s) {
-          const int j = PAIR ? s >> 1 : s, p = s & 1;
-          const int c = cnt + 2 * j, st = c % C::STAGES;
-          if (s < (PAIR ? 2 : 1) && !mbar_wait(smem_u32(&q_full[p]), nseg & 1, abort)) return false;
-          if ((!PAIR || p == 0) && !mbar_wait(smem_u32(&full[st]), (c / C::STAGES) & 1, abort)) return false;
+      if (seg.n == 0) break;
+      const int n = __shfl_sync(0xffffffffu, seg.n, 0);
+      const int steps = PAIR ? 2 * n : n;
+      auto issue_s = [&](int s) {
+        const int j = PAIR ? s >> 1 : s, p = s & 1;
+        const int c = cnt + 2 * j, st = c % C::STAGES;
+        if (s < (PAIR ? 2 : 1)) (void)mbar_wait(smem_u32(&q_full[p]), nseg & 1, abort);
+        if (!PAIR || p == 0) (void)mbar_wait(smem_u32(&full[st]), (c / C::STAGES) & 1, abort);
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < DH / 64; ++h)
+          tc_mma4(tmem + p * 128, (uint32_t)dq + (((PAIR ? p * C::TILE : 0) + h * C::BOX) >> 4),
+                  (uint32_t)dk + ((st * C::TILE + h * C::BOX) >> 4), (uint32_t)(dk >> 32), idS, h > 0);
+        if (!PAIR || p == 1) tc_commit_elect(smem_u32(&empty[st]));
+        tc_commit_elect(smem_u32(&s_full[p]));
+      };
+      auto issue_pv = [&](int s) {
+        const int j = PAIR ? s >> 1 : s, p = s & 1;
+        const int c = cnt + 2 * j + 1, st = c % C::STAGES;
+        const uint32_t ph = (p ? pc1++ : pc0++) & 1;
+        (void)mbar_wait(smem_u32(&full[st]), (c / C::STAGES) & 1, abort);
+        // the block's second 64 keys are ready first
+#pragma unroll
+        for (int h = 1; h >= 0; --h) {
+          (void)mbar_wait(smem_u32(h ? &p_half[p] : &p_full[p]), ph, abort);
           tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < DH / 16; ++k) {
-            const uint32_t off = (k >> 2) * C::BOX + (k & 3) * 32;
-            tc_mma(tmem + p * 128, desc_sw128(smem_u32(sQ + (PAIR ? p * C::TILE : 0)) + off),
-                   desc_sw128(smem_u32(sKV + st * C::TILE) + off), idS, k > 0);
-          }
-          if (!PAIR || p == 1) tc_commit(smem_u32(&empty[st]));
-          tc_commit(smem_u32(&s_full[p]));
-          return true;
-        };
-        auto issue_pv = [&](int s) {
-          const int j = PAIR ? s >> 1 : s, p = s & 1;
-          const int c = cnt + 2 * j + 1, st = c % C::STAGES;
-          if (!mbar_wait(smem_u32(&full[st]), (c / C::STAGES) & 1, abort)) return false;
-          // the block's second 64 keys are ready first
-#pragma unroll
-          for (int h = 1; h >= 0; --h) {
-            if (!mbar_wait(smem_u32(h ? &p_half[p] : &p_full[p]), pc[p] & 1, abort)) return false;
-            tc_fence_after();
-#pragma unroll
-            for (int k = h * 4; k < h * 4 + 4; ++k)
-              tc_mma_ts(tmem + C::O_COL + p * 128, tmem + p * 128 + C::P_COL + k * 8,
-                        desc_sw128_mn(smem_u32(sKV + st * C::TILE) + k * 2048, C::BOX), idO,
-                        s >= 2 || k != 4);
-          }
-          ++pc[p];
-          if (!PAIR || p == 1) tc_commit(smem_u32(&empty[st]));
-          if (s + 2 >= steps) tc_commit(smem_u32(&o_full[p]));
-          return true;
-        };
-        for (int s = 0; ok && s < min(2, steps); ++s) ok = issue_s(s);
-        for (int s = 0; ok && s < steps; ++s) {
-          ok = issue_pv(s);
-          if (ok && s + 2 < steps) ok = issue_s(s + 2);
+          tc_mma4_ts(tmem + C::O_COL + p * 128, tmem + p * 128 + C::P_COL + h * 32,
+                     (uint32_t)dv + ((st * C::TILE + h * 64 * 128) >> 4), (uint32_t)(dv >> 32), idO,
+                     s >= 2 || h == 0);
         }
+        if (!PAIR || p == 1) tc_commit_elect(smem_u32(&empty[st]));
+        if (s + 2 >= steps) tc_commit_elect(smem_u32(&o_full[p]));
+      };
+      issue_s(0);
+      if (steps > 1) issue_s(1);
+      for (int s = 0; s < steps; ++s) {
+        issue_pv(s);
+        if (s + 2 < steps) issue_s(s + 2);
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      cnt += 2 * seg.n;
+      cnt += 2 * n;
       seg.done(a);
     }
   } else if (warp >= 4) {
@@ -245,8 +248,9 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     int cnt = 0;                                        // ring entries of earlier segments
     const int np = CT_KB >> a.c.ps_log2;
     const uint32_t all_pages = (1u << np) - 1u;
-    for (long long u = u0; u < u1; u += seg.n) {
+    for (long long u = u0; u < u1; u += seg.nv) {
       seg.at(a, u, u1);
+      if (seg.n == 0) break;
       const SeenBlocks<CT_KB> blocks(seg.seen);
       const int all = seg.all;
       const int xw = seg.x0 + (PAIR ? p * a.rt : 0);    // this warpgroup's first packed row
@@ -292,8 +296,8 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
               if (!row_seen(seg.seen, kr)) {
                 uint8_t* v = sKV + (ring % C::STAGES) * C::TILE + r * 128;
 #pragma unroll
-                for (int c = 0; c < DH / 8; ++c)
-                  *(uint4*)(v + (c >> 3) * C::BOX + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < DH / 8; ++c)        // neighbouring rows on different banks
+                  *(uint4*)(v + (c >> 3) * C::BOX + (((c + r) & 7) << 4)) = make_uint4(0, 0, 0, 0);
               }
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
@@ -399,7 +403,8 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
       if (!PAIR && p >= seg.n) mbar_arrive(smem_u32(&q_empty[0]));   // it had no block
       // ---- the segment's result, one row a thread
       const bool whole = seg.j0 == 0 && seg.n == seg.nb;
-      const size_t prt = ((size_t)blockIdx.x * 2 + (u == u0 ? 0 : 1)) * QT + (PAIR ? p * 128 : 0) + r;
+      const size_t prt = (size_t)blockIdx.x * 2 + (u == u0 ? 0 : 1);   // its slot
+      const int pr = (PAIR ? p * 128 : 0) + r;
       const int t = seg.row0 + qi;
       auto put = [&](int c0, const uint32_t* o, float f) {   // 32 columns
         if (!live) return;
@@ -414,14 +419,15 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             *(uint4*)(dst + i) = make_uint4(v[0], v[1], v[2], v[3]);
           }
         } else {
+          // [column][row], so that a warp's store is one line
+          float* const dst = a.part + (prt * DH + c0) * QT + pr;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *(uint4*)(a.part + prt * DH + c0 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int i = 0; i < 32; ++i) dst[(size_t)i * QT] = __uint_as_float(o[i]);
         }
       };
       auto stats = [&](float mm, float ll) {
         if (!live) return;
-        if (!whole) a.part_ml[prt] = make_float2(mm, ll);
+        if (!whole) a.part_ml[prt * QT + pr] = make_float2(mm, ll);
         else if (a.lse)
           a.lse[(size_t)t * a.n_heads + hq] =
               ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;

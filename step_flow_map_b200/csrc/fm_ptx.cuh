@@ -216,14 +216,77 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// As tc_mma with A (bf16, two per 32-bit column, row = lane) in TMEM.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                          uint32_t idesc, uint32_t accum) {
+// Four MMAs of a 64-wide stretch of the reduction, issued by one lane the
+// warp elects (the warp runs converged, so descriptors stay in uniform
+// registers: issued from a one-lane branch, an MMA cost about 150 cycles of
+// moves against the 64 it runs).  a_lo, b_lo: low words of the first
+// descriptors, hi: the high word they share.  K-major operands step by 32
+// bytes per MMA.
+__device__ __forceinline__ void tc_mma4(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                        uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred e, p, q;\n\t.reg .b32 al, bl;\n\t.reg .b64 da, db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accum)
+      "setp.eq.u32 q, 0, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+      "add.u32 al, %1, 2;\n\t"
+      "add.u32 bl, %2, 2;\n\t"
+      "mov.b64 da, {al, %5};\n\t"
+      "mov.b64 db, {bl, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, q;\n\t"
+      "add.u32 al, %1, 4;\n\t"
+      "add.u32 bl, %2, 4;\n\t"
+      "mov.b64 da, {al, %5};\n\t"
+      "mov.b64 db, {bl, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, q;\n\t"
+      "add.u32 al, %1, 6;\n\t"
+      "add.u32 bl, %2, 6;\n\t"
+      "mov.b64 da, {al, %5};\n\t"
+      "mov.b64 db, {bl, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, q;\n\t"
+      "}"
+      :
+      : "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accum), "r"(hi)
+      : "memory");
+}
+// The same with A in TMEM (bf16, two per 32-bit column, row = lane: 8 columns
+// per MMA) and an MN-major B (16 rows of 128 bytes per MMA).
+__device__ __forceinline__ void tc_mma4_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                           uint32_t hi, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, q;\n\t.reg .b32 al, bl;\n\t.reg .b64 db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.u32 q, 0, 0;\n\t"
+      "mov.b32 al, %1;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], db, %3, p;\n\t"
+      "add.u32 al, %1, 8;\n\t"
+      "add.u32 bl, %2, 128;\n\t"
+      "mov.b64 db, {bl, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], db, %3, q;\n\t"
+      "add.u32 al, %1, 16;\n\t"
+      "add.u32 bl, %2, 256;\n\t"
+      "mov.b64 db, {bl, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], db, %3, q;\n\t"
+      "add.u32 al, %1, 24;\n\t"
+      "add.u32 bl, %2, 384;\n\t"
+      "mov.b64 db, {bl, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [al], db, %3, q;\n\t"
+      "}"
+      :
+      : "r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accum), "r"(hi)
+      : "memory");
+}
+// tc_commit by the lane the warp elects.
+__device__ __forceinline__ void tc_commit_elect(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 // Shared-memory matrix descriptor of an MN-major operand written by TMA with
