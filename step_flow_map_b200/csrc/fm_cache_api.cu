@@ -183,7 +183,7 @@ struct AttnPlan {
   enum { DECODE, TC_ONE, TC_PAIR, SIMT } kind = SIMT;
   int qt = 0, rt = 0, tile_rows = 0, ov = 0, grid = 0;   // rows of a partial; see CacheAttnArgs
   int64_t tiles = 0;
-  size_t o_first = 0, o_tile = 0, o_lse = 0, o_ml = 0, o_part = 0, total = 0;
+  size_t o_first = 0, o_tile = 0, o_join = 0, o_lse = 0, o_ml = 0, o_part = 0, total = 0;
 };
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -216,16 +216,23 @@ fm_status plan_attention(const fm_paged_cache* c, const fm_attention_args* a, At
       p->kind = pair ? AttnPlan::TC_PAIR : AttnPlan::TC_ONE;
       p->qt = pair ? 256 : 128;
       p->tile_rows = pair ? 2 * p->rt : p->rt;
-      p->ov = 2;
+      p->ov = 4;
       p->grid = sms;
     }
   }
   p->tiles = ((int64_t)a->T * G) / p->tile_rows + a->B;
+  // units are 31-bit numbers
+  const int64_t kb = p->kind == AttnPlan::TC_ONE || p->kind == AttnPlan::TC_PAIR ? fm::CT_KB : fm::CD_KB;
+  if (p->tiles * c->n_kv_heads >= 0x7fffffff / (a->max_kv / kb + p->ov + 2))
+    return set_err(FM_ERR_UNSUPPORTED, "T=%d rows over max_kv %d: more than 2^31 blocks of work", a->T,
+                   a->max_kv);
   size_t at = 256;
   p->o_first = at;
-  at = up256(at + (size_t)(p->tiles + 1) * sizeof(long long));
+  at = up256(at + (size_t)(p->tiles + 1) * sizeof(int));
   p->o_tile = at;
   at = up256(at + (size_t)p->tiles * 2 * sizeof(int4));
+  p->o_join = at;
+  at = up256(at + (size_t)p->grid * 2 * sizeof(int4));
   p->o_lse = at;
   if (a->accumulate) at = up256(at + (size_t)a->T * a->n_heads * sizeof(float));
   p->o_ml = at;
@@ -245,8 +252,8 @@ fm_status launch_simt(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_
   FM_LAUNCH_OK("cache attention", fm::launch_pdl(fm::k_cache_attn_simt<T, DH, QT>, dim3(p.grid),
                                                  dim3(fm::CS_THREADS), C::SMEM, st, k));
   FM_LAUNCH_OK("cache attention join",
-               fm::launch_pdl(fm::k_cache_join<T, DH, QT>, dim3(p.grid - 1, QT / 4),
-                              dim3(fm::CJ_THREADS), 0, st, k, p.grid));
+               fm::launch_pdl(fm::k_cache_join_rows<T, DH, QT>, dim3(p.grid - 1, QT),
+                              dim3(fm::CJ_THREADS), 0, st, k));
   return FM_OK;
 }
 
@@ -261,9 +268,9 @@ fm_status launch_decode(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStrea
                                                  dim3(fm::CD_THREADS), C::SMEM, st, k));
   if (grid > 1)
     FM_LAUNCH_OK("cache attention join",
-                 fm::launch_pdl(fm::k_cache_decode_join<DH>,
-                                dim3(grid - 1, (unsigned)((k.max_rows * k.G + 3) / 4)),
-                                dim3(fm::CD_THREADS), 0, st, k, grid));
+                 fm::launch_pdl(fm::k_cache_join_rows<bf16, DH, fm::CD_QT>,
+                                dim3(grid - 1, (unsigned)(k.max_rows * k.G)), dim3(fm::CJ_THREADS), 0,
+                                st, k));
   return FM_OK;
 }
 
@@ -308,8 +315,8 @@ fm_status launch_tc(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_t 
   FM_LAUNCH_OK("cache attention", fm::launch_pdl(kernel, dim3(p.grid), dim3(fm::CT_THREADS), C::SMEM,
                                                  st, mk, mv, mq, k));
   FM_LAUNCH_OK("cache attention join",
-               fm::launch_pdl(fm::k_cache_join<bf16, DH, QT>, dim3(p.grid - 1, QT / 32),
-                              dim3(fm::CJ_THREADS), 0, st, k, p.grid));
+               fm::launch_pdl(fm::k_cache_join_cols<DH, QT>, dim3(p.grid - 1, QT / 32),
+                              dim3(fm::CJ_THREADS), 0, st, k));
   return FM_OK;
 }
 
@@ -383,8 +390,9 @@ extern "C" fm_status fm_cache_attention(const fm_paged_cache* c, const fm_attent
   char* w = (char*)ws;
   k.lse = a->lse ? a->lse : a->accumulate ? (float*)(w + p.o_lse) : nullptr;
   k.plan_n = (int*)w;
-  k.plan_first = (long long*)(w + p.o_first);
+  k.plan_first = (int*)(w + p.o_first);
   k.plan_tile = (int4*)(w + p.o_tile);
+  k.plan_join = (int4*)(w + p.o_join);
   k.part_ml = (float2*)(w + p.o_ml);
   k.part = (float*)(w + p.o_part);
   cudaStream_t st = (cudaStream_t)stream;

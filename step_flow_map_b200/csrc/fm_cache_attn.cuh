@@ -33,9 +33,10 @@ struct CacheAttnArgs {
   float* lse;                      // or null
   // workspace
   int* plan_n;                     // [0]: number of tiles, [1]: status of the call
-  long long* plan_first;           // [tiles + 1]: first unit of each tile, heads apart
+  int* plan_first;                 // [tiles + 1]: first unit of each tile, heads apart
   int4* plan_tile;                 // [tiles][2]: (b, first packed row, first new row, packed rows
                                    //   of the sequence), (s_end, lo, hi, position of new row 0)
+  int4* plan_join;                 // [grid][2], see JoinItem
   float* part;                     // [grid][2][QT][DH]
   float2* part_ml;                 // [grid][2][QT]: (max, sum), log2 units
 };
@@ -87,7 +88,7 @@ constexpr int CP_THREADS = 1024;
 template <int KB>
 __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a) {
   __shared__ int s_tiles[257];
-  __shared__ long long s_warp[32];
+  __shared__ int s_warp[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int QT = a.tile_rows;
   pdl_wait();
@@ -99,18 +100,27 @@ __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a
   }
   if (tid == 0) s_tiles[0] = 0;
   __syncthreads();
-  for (int o = 1; o < 256; o <<= 1) {
-    int v = 0;
-    if (tid < 256 && tid >= o) v = s_tiles[tid + 1 - o];
-    __syncthreads();
-    if (tid < 256) s_tiles[tid + 1] += v;
-    __syncthreads();
+  if (warp == 0) {                 // prefix sum, eight sequences a lane
+    int v[8], sum = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += v[k] = s_tiles[lane * 8 + k + 1];
+    int at = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += y;
+    }
+    at -= sum;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s_tiles[lane * 8 + k + 1] = at += v[k];
   }
+  __syncthreads();
   const int E = s_tiles[256];
-  long long base = 0;
+  int base = 0;
   for (int e0 = 0; e0 < E; e0 += CP_THREADS) {
     const int e = e0 + tid;
-    long long nb = 0;                // units: the blocks, and the tile's overhead
+    int nb = 0;                      // units: the blocks, and the tile's overhead
     if (e < E) {
       int b = 0;                   // largest b with s_tiles[b] <= e
       for (int step = 128; step > 0; step >>= 1)
@@ -123,16 +133,16 @@ __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a
       a.plan_tile[2 * e] = make_int4(b, tile * QT, s.first, rows);
       a.plan_tile[2 * e + 1] = make_int4(r.s_end, r.lo, r.hi, s.L - s.n);
     }
-    long long x = nb;
+    int x = nb;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     __syncthreads();
     if (lane == 31) s_warp[warp] = x;
     __syncthreads();
-    long long add = base, sum = 0;
+    int add = base, sum = 0;
     for (int i = 0; i < 32; ++i) {
       if (i < warp) add += s_warp[i];
       sum += s_warp[i];
@@ -150,21 +160,23 @@ __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a
 // The run of units of CTA c of `grid`, and the tile a unit falls in.  Units of
 // a tile: for head 0 `ov` units that stand for its start and end and then its
 // blocks, then the same for head 1, and so on.
+// There are fewer than 2^31 units (checked by the host from the bounds it was
+// given).
 struct WorkRun {
-  long long N;
-  int g;                           // CTAs that have work
-  __device__ __forceinline__ long long start(int c) const { return N * c / g; }
-  __device__ __forceinline__ int cta_of(long long u) const { return (int)(((u + 1) * g - 1) / N); }
+  int N, g, q, rem;                // units; CTAs that have work; N = g q + rem
+  __device__ __forceinline__ WorkRun(int N_, int grid) : N(N_), g(max(1, min(grid, N_))) {
+    q = N / g;
+    rem = N - q * g;
+  }
+  __device__ __forceinline__ int start(int c) const { return q * c + min(c, rem); }
+  __device__ __forceinline__ int cta_of(int u) const {
+    const int t = rem * (q + 1);
+    return u < t ? u / (q + 1) : rem + (u - t) / q;
+  }
 };
-__device__ __forceinline__ WorkRun work_run(const CacheAttnArgs& a, int E, int grid) {
-  WorkRun w;
-  w.N = a.plan_first[E] * a.c.n_kv;
-  w.g = (int)min((long long)grid, w.N);
-  return w;
-}
 // Largest e with plan_first[e] n_kv <= u; every lane of the warp takes part,
 // 32 probes a round.
-__device__ __forceinline__ int find_tile(const CacheAttnArgs& a, int E, long long u) {
+__device__ __forceinline__ int find_tile(const CacheAttnArgs& a, int E, int u) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = E;               // the answer lies in [lo, lo + n)
   while (n > 1) {
@@ -176,6 +188,20 @@ __device__ __forceinline__ int find_tile(const CacheAttnArgs& a, int E, long lon
     lo += k * step;
   }
   return lo;
+}
+// What the second kernel joins at the start of run c: the tile that run c0 =
+// c - 1 began (its partial in slot slot0) and runs .. last continue, when run
+// c's start is the first to fall among its blocks; else c0 = -1.  Every CTA
+// writes its own entry: {c0, last, slot0, packed rows of the sequence}, {first
+// new row, head, first packed row, -}.
+__device__ __forceinline__ void put_join(const CacheAttnArgs& a, const WorkRun& w, int c, int first,
+                                         int units, int row0, int g, int x0, int all) {
+  const int u = w.start(c), real = first + a.ov;
+  int c0 = -1;
+  if (c > 0 && c < w.g && u > real && w.start(c - 1) <= real) c0 = c - 1;
+  a.plan_join[2 * c] = make_int4(c0, c0 < 0 ? 0 : w.cta_of(first + units - 1),
+                                 c0 < 0 || w.start(c0) >= first ? 0 : 1, all);
+  a.plan_join[2 * c + 1] = make_int4(row0, g, x0, 0);
 }
 
 // ------------------------------------------------------------------ CUDA-core kernel (fp32)
@@ -209,23 +235,24 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
   pdl_wait();
   pdl_trigger();
   const int E = a.plan_n[0];
-  if (E == 0) return;
-  const WorkRun w = work_run(a, E, gridDim.x);
-  if ((int)blockIdx.x >= w.g) return;
-  long long u = w.start(blockIdx.x);
-  const long long u1 = w.start(blockIdx.x + 1);
-  const long long u0 = u;
+  const WorkRun w(a.plan_first[E] * a.c.n_kv, gridDim.x);
+  if ((int)blockIdx.x >= w.g || w.N == 0) {
+    if (tid == 0) a.plan_join[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  int u = w.start(blockIdx.x);
+  const int u1 = w.start(blockIdx.x + 1), u0 = u;
   int e = find_tile(a, E, u);
   while (u < u1) {
-    const long long t0 = a.plan_first[e];
-    const int nb = (int)(a.plan_first[e + 1] - t0);
-    const int g = (int)((u - t0 * a.c.n_kv) / nb), j0 = (int)((u - t0 * a.c.n_kv) % nb);
-    const int j1 = (int)min((long long)nb, j0 + (u1 - u));
+    const int t0 = a.plan_first[e], nb = a.plan_first[e + 1] - t0;
+    const int g = (u - t0 * a.c.n_kv) / nb, j0 = u - t0 * a.c.n_kv - g * nb;
+    const int j1 = min(nb, j0 + (u1 - u));
     const int4 pt = a.plan_tile[2 * e], ps = a.plan_tile[2 * e + 1];
     const int b = pt.x;
     const SeenRows seen = {ps.x, ps.y, ps.z};
     const SeenBlocks<CS_KB> blocks(seen);
     const int x0 = pt.y, row0 = pt.z, rows = min(QT, pt.w - x0);
+    if (u == u0 && tid == 0) put_join(a, w, blockIdx.x, u - j0, nb, row0, g, x0, pt.w);
     __syncthreads();
     for (int i = tid; i < QT * (DH / VE); i += CS_THREADS) {
       const int r = i / (DH / VE), c = (i % (DH / VE)) * VE;
@@ -368,22 +395,34 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
       }
     }
     u += j1 - j0;
-    if (u - t0 * a.c.n_kv >= (long long)nb * a.c.n_kv) ++e;
+    if (u - t0 * a.c.n_kv >= nb * a.c.n_kv) ++e;
   }
 }
 
 // ------------------------------------------------------------------ join
-// The partials of a split tile, one warp per packed row.  CTA x looks at the
-// start of run x: it joins the tile that run x - 1 began and left, unless an
-// earlier boundary already fell in that tile.
+// The partials of split tiles, in run order.  blockIdx.x is the entry of
+// plan_join (1 .. grid - 1).  Bound: latency, one round of loads for the
+// entry, one for the sums, one for the partials.
 constexpr int CJ_THREADS = 128;
-// Row x of a tile whose partials are runs c0 .. last (run c0's in slot slot0,
-// the others' in slot 0), one warp, to output row t and head h.
-template <typename T, int DH>
-__device__ __forceinline__ void join_row(const CacheAttnArgs& a, int c0, int last, int slot0, int qt,
-                                         int x, int t, int h) {
-  const int lane = threadIdx.x & 31;
-  auto at = [&](int i) { return ((size_t)i * 2 + (i == c0 ? slot0 : 0)) * qt + x; };
+
+__device__ __forceinline__ void join_store_lse(const CacheAttnArgs& a, int t, int h, float m, float l) {
+  if (a.lse)
+    a.lse[(size_t)t * a.n_heads + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Partials [row][column] (tiles of at most 64 rows): a CTA per packed row, its
+// warps take every fourth run.
+template <typename T, int DH, int QT>
+__global__ void __launch_bounds__(CJ_THREADS) k_cache_join_rows(const CacheAttnArgs a) {
+  constexpr int W = CJ_THREADS / 32;
+  __shared__ float s_l[W], s_o[W][DH];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const int4 ja = a.plan_join[2 * blockIdx.x + 2], jb = a.plan_join[2 * blockIdx.x + 3];
+  const int c0 = ja.x, last = ja.y, r = blockIdx.y, x = jb.z + r;
+  if (c0 < 0 || x >= ja.w) return;
+  auto at = [&](int i) { return ((size_t)i * 2 + (i == c0 ? ja.z : 0)) * QT + r; };
   float m = -INFINITY;
   for (int i = c0 + lane; i <= last; i += 32) m = fmaxf(m, a.part_ml[at(i)].x);
   m = warp_max(m);
@@ -392,7 +431,7 @@ __device__ __forceinline__ void join_row(const CacheAttnArgs& a, int c0, int las
 #pragma unroll
   for (int k = 0; k < DH / 32; ++k) o[k] = 0.f;
 #pragma unroll 8
-  for (int i = c0; i <= last; ++i) {
+  for (int i = c0 + warp; i <= last; i += W) {
     const size_t p = at(i);
     const float2 ml = a.part_ml[p];
     const float f = exp2f(ml.x - ref);
@@ -400,73 +439,59 @@ __device__ __forceinline__ void join_row(const CacheAttnArgs& a, int c0, int las
 #pragma unroll
     for (int k = 0; k < DH / 32; ++k) o[k] = fmaf(a.part[p * DH + lane + 32 * k], f, o[k]);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (lane == 0) s_l[warp] = l;
 #pragma unroll
-  for (int k = 0; k < DH / 32; ++k)
-    ((T*)a.out)[t * a.os + h * DH + lane + 32 * k] = from_f<T>(o[k] * inv);
-  if (a.lse && lane == 0)
-    a.lse[(size_t)t * a.n_heads + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  for (int k = 0; k < DH / 32; ++k) s_o[warp][lane + 32 * k] = o[k];
+  __syncthreads();
+  const int col = threadIdx.x;
+  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  const int t = jb.x + x / a.G, h = jb.y * a.G + x % a.G;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (col < DH)
+    ((T*)a.out)[t * a.os + h * DH + col] =
+        from_f<T>(((s_o[0][col] + s_o[1][col]) + (s_o[2][col] + s_o[3][col])) * inv);
+  if (threadIdx.x == 0) join_store_lse(a, t, h, m, l);
 }
 
-template <typename T, int DH, int QT>
-__global__ void __launch_bounds__(CJ_THREADS) k_cache_join(const CacheAttnArgs a, int grid) {
+// Partials [column][row] (the 128-row tiles): a lane per row, a warp per
+// DH / 4 columns.  Partial row r is row r % 128 of half tile r / 128.
+template <int DH, int QT>
+__global__ void __launch_bounds__(CJ_THREADS) k_cache_join_cols(const CacheAttnArgs a) {
+  constexpr int COLS = DH / (CJ_THREADS / 32);
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x + 1;
-  const int E = a.plan_n[0];
-  if (E == 0) return;
-  const WorkRun w = work_run(a, E, grid);
-  if (c >= w.g) return;
-  const long long u = w.start(c);
-  const int e = find_tile(a, E, u);
-  const long long t0 = a.plan_first[e];
-  const int nb = (int)(a.plan_first[e + 1] - t0);
-  const int g = (int)((u - t0 * a.c.n_kv) / nb);
-  const long long first = t0 * a.c.n_kv + (long long)g * nb;
-  // no block lies before u, or an earlier boundary already split the tile
-  if (u <= first + a.ov || w.start(c - 1) > first + a.ov) return;
-  const int last = w.cta_of(first + nb - 1);
-  const int slot0 = w.start(c - 1) >= first ? 0 : 1;   // did run c - 1 begin with the tile?
-  const int4 pt = a.plan_tile[2 * e];
-  if constexpr (QT < 128) {
-    const int r = blockIdx.y * (CJ_THREADS / 32) + (threadIdx.x >> 5), x = pt.y + r;
-    if (r >= QT || x >= pt.w) return;
-    join_row<T, DH>(a, c - 1, last, slot0, QT, r, pt.z + x / a.G, g * a.G + x % a.G);
-  } else {
-    // partials stored [column][row]: a lane per row, a warp per DH / 4 columns;
-    // partial row r is row r % 128 of half tile r / 128
-    constexpr int COLS = DH / (CJ_THREADS / 32);
-    const int r = blockIdx.y * 32 + (threadIdx.x & 31), c0 = (threadIdx.x >> 5) * COLS;
-    const int x = pt.y + (r >> 7) * a.rt + (r & 127);
-    if ((r & 127) >= a.rt || x >= pt.w) return;
-    float m = -INFINITY, l = 0.f, o[COLS];
-    auto slot = [&](int i) { return (size_t)i * 2 + (i == c - 1 ? slot0 : 0); };
+  const int4 ja = a.plan_join[2 * blockIdx.x + 2], jb = a.plan_join[2 * blockIdx.x + 3];
+  const int first = ja.x, last = ja.y;
+  const int r = blockIdx.y * 32 + (threadIdx.x & 31), c0 = (threadIdx.x >> 5) * COLS;
+  const int x = jb.z + (r >> 7) * a.rt + (r & 127);
+  if (first < 0 || (r & 127) >= a.rt || x >= ja.w) return;
+  float m = -INFINITY, l = 0.f, o[COLS];
+  auto slot = [&](int i) { return (size_t)i * 2 + (i == first ? ja.z : 0); };
 #pragma unroll 4
-    for (int i = c - 1; i <= last; ++i) m = fmaxf(m, a.part_ml[slot(i) * QT + r].x);
-    const float ref = m == -INFINITY ? 0.f : m;
+  for (int i = first; i <= last; ++i) m = fmaxf(m, a.part_ml[slot(i) * QT + r].x);
+  const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (int k = 0; k < COLS; ++k) o[k] = 0.f;
-    for (int i = c - 1; i <= last; ++i) {
-      const float2 ml = a.part_ml[slot(i) * QT + r];
-      const float f = exp2f(ml.x - ref);
-      l = fmaf(ml.y, f, l);
-      const float* p = a.part + (slot(i) * DH + c0) * QT + r;
+  for (int k = 0; k < COLS; ++k) o[k] = 0.f;
+#pragma unroll 2
+  for (int i = first; i <= last; ++i) {
+    const float2 ml = a.part_ml[slot(i) * QT + r];
+    const float f = exp2f(ml.x - ref);
+    l = fmaf(ml.y, f, l);
+    const float* p = a.part + (slot(i) * DH + c0) * QT + r;
 #pragma unroll
-      for (int k = 0; k < COLS; ++k) o[k] = fmaf(p[(size_t)k * QT], f, o[k]);
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int t = pt.z + x / a.G, h = g * a.G + x % a.G;
-    T* dst = (T*)a.out + t * a.os + h * DH + c0;
-#pragma unroll
-    for (int k = 0; k < COLS; k += Vec16<T>::N) {
-      float v[Vec16<T>::N];
-#pragma unroll
-      for (int z = 0; z < Vec16<T>::N; ++z) v[z] = o[k + z] * inv;
-      *(uint4*)(dst + k) = Vec16<T>::pack(v);
-    }
-    if (a.lse && c0 == 0)
-      a.lse[(size_t)t * a.n_heads + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    for (int k = 0; k < COLS; ++k) o[k] = fmaf(p[(size_t)k * QT], f, o[k]);
   }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int t = jb.x + x / a.G, h = jb.y * a.G + x % a.G;
+  bf16* dst = (bf16*)a.out + t * a.os + h * DH + c0;
+#pragma unroll
+  for (int k = 0; k < COLS; k += 8) {
+    float v[8];
+#pragma unroll
+    for (int z = 0; z < 8; ++z) v[z] = o[k + z] * inv;
+    *(uint4*)(dst + k) = Vec16<bf16>::pack(v);
+  }
+  if (c0 == 0) join_store_lse(a, t, h, m, l);
 }
 
 // ------------------------------------------------------------------ weights

@@ -66,27 +66,21 @@ __device__ __forceinline__ void decode_scan(const CacheAttnArgs& a, DecodeSeqs& 
   if (tid == 0) s.first[0] = 0;
   __syncthreads();
 }
-__device__ __forceinline__ WorkRun decode_run(const CacheAttnArgs& a, const DecodeSeqs& s, int grid) {
-  WorkRun w;
-  w.N = (long long)s.first[256] * a.c.n_kv;
-  w.g = (int)min((long long)grid, w.N);
-  return w;
-}
-__device__ __forceinline__ int decode_find(const CacheAttnArgs& a, const DecodeSeqs& s, long long u) {
+__device__ __forceinline__ int decode_find(const CacheAttnArgs& a, const DecodeSeqs& s, int u) {
   int b = 0;
 #pragma unroll
   for (int step = 128; step > 0; step >>= 1)
-    if ((long long)s.first[b + step] * a.c.n_kv <= u) b += step;
+    if (s.first[b + step] * a.c.n_kv <= u) b += step;
   return b;
 }
 
 // A unit of the CTA's run: block j of head g of sequence b.
 struct DecodeCursor {
   int b, g, j, nb;
-  __device__ __forceinline__ void seek(const CacheAttnArgs& a, const DecodeSeqs& s, long long u) {
+  __device__ __forceinline__ void seek(const CacheAttnArgs& a, const DecodeSeqs& s, int u) {
     b = decode_find(a, s, u);
     nb = s.first[b + 1] - s.first[b];
-    const int at = (int)(u - (long long)s.first[b] * a.c.n_kv);
+    const int at = u - s.first[b] * a.c.n_kv;
     g = at / nb;
     j = at - g * nb;
   }
@@ -130,16 +124,20 @@ __global__ void __launch_bounds__(CD_THREADS, 2) k_cache_decode(const CacheAttnA
   pdl_trigger();
   if (blockIdx.x == 0 && tid == 0) a.plan_n[1] = 0;
   decode_scan<CD_KB>(a, s, s_scan);
-  const WorkRun w = decode_run(a, s, gridDim.x);
-  if ((int)blockIdx.x >= w.g) return;
-  const long long u0 = w.start(blockIdx.x);
-  const int count = (int)(w.start(blockIdx.x + 1) - u0);
+  const WorkRun w(s.first[256] * a.c.n_kv, gridDim.x);
+  if ((int)blockIdx.x >= w.g || w.N == 0) {
+    if (tid == 0) a.plan_join[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  const int u0 = w.start(blockIdx.x), count = w.start(blockIdx.x + 1) - u0;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smb) + warp * C::RING;
   float* merge = (float*)(smb + 4 * C::RING);
 
   DecodeCursor ld, cu;
   ld.seek(a, s, u0);
   cu = ld;
+  if (tid == 0)
+    put_join(a, w, blockIdx.x, u0 - ld.j, ld.nb, s.row0[ld.b], ld.g, 0, s.n[ld.b] * a.G);
   auto tile_row = [&](const DecodeCursor& c) {
     const SeenRows v = {s.s_end[c.b], s.lo[c.b], s.hi[c.b]};
     return SeenBlocks<CD_KB>(v).row(c.j) + 16 * warp;
@@ -366,30 +364,6 @@ __global__ void __launch_bounds__(CD_THREADS, 2) k_cache_decode(const CacheAttnA
     }
   }
   cp_wait<0>();
-}
-
-// Joins the partials of split tiles (see k_cache_join): a warp per packed row.
-template <int DH>
-__global__ void __launch_bounds__(CD_THREADS) k_cache_decode_join(const CacheAttnArgs a, int grid) {
-  __shared__ DecodeSeqs s;
-  __shared__ int s_scan[4];
-  pdl_wait();
-  pdl_trigger();
-  decode_scan<CD_KB>(a, s, s_scan);
-  const WorkRun w = decode_run(a, s, grid);
-  const int c = blockIdx.x + 1;
-  if (c >= w.g) return;
-  const long long u = w.start(c);
-  const int b = decode_find(a, s, u);
-  const int nb = s.first[b + 1] - s.first[b];
-  const int g = (int)((u - (long long)s.first[b] * a.c.n_kv) / nb);
-  const long long first = (long long)s.first[b] * a.c.n_kv + (long long)g * nb;
-  if (first == u || w.start(c - 1) > first) return;
-  const int last = w.cta_of(first + nb - 1);
-  const int slot0 = w.start(c - 1) == first ? 0 : 1;
-  const int x = blockIdx.y * (CD_THREADS / 32) + (threadIdx.x >> 5);
-  if (x >= s.n[b] * a.G) return;
-  join_row<bf16, DH>(a, c - 1, last, slot0, CD_QT, x, s.row0[b] + x / a.G, g * a.G + x % a.G);
 }
 
 }  // namespace fm

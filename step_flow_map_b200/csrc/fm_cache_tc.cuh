@@ -48,14 +48,13 @@ struct CtCfg {
 struct TileSeg {
   int e, g, nv, j0, n, nb, b, x0, row0, all, p0;   // row0: first new row; all: its packed rows;
   SeenRows seen;                                   //   p0: position of its first new row
-  __device__ __forceinline__ void at(const CacheAttnArgs& a, long long u, long long u1) {
-    const long long t0 = a.plan_first[e];
-    const int units = (int)(a.plan_first[e + 1] - t0);
+  __device__ __forceinline__ void at(const CacheAttnArgs& a, int u, int u1) {
+    const int t0 = a.plan_first[e], units = a.plan_first[e + 1] - t0;
     const int4 t = a.plan_tile[2 * e], s = a.plan_tile[2 * e + 1];
-    const unsigned d = (unsigned)(u - t0 * a.c.n_kv);   // < units x heads of one tile
-    g = (int)(d / (unsigned)units);
-    const int v0 = (int)(d - (unsigned)g * (unsigned)units);
-    nv = (int)min((long long)(units - v0), u1 - u);
+    const int d = u - t0 * a.c.n_kv;
+    g = d / units;
+    const int v0 = d - g * units;
+    nv = min(units - v0, u1 - u);
     nb = units - a.ov;
     j0 = max(0, v0 - a.ov);
     n = max(0, v0 + nv - a.ov) - j0;
@@ -123,21 +122,18 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   const int E = a.plan_n[0];
-  WorkRun w = {0, 0};
-  if (E > 0) w = work_run(a, E, gridDim.x);
-  const bool active = (int)blockIdx.x < w.g;
-  const long long u0 = active ? w.start(blockIdx.x) : 0;
-  const long long u1 = active ? w.start(blockIdx.x + 1) : 0;
+  const WorkRun w(a.plan_first[E] * a.c.n_kv, gridDim.x);
+  const bool active = (int)blockIdx.x < w.g && w.N > 0;
+  const int u0 = active ? w.start(blockIdx.x) : 0, u1 = active ? w.start(blockIdx.x + 1) : 0;
   TileSeg seg;
-  seg.e = active && warp != 2 && warp != 3 ? find_tile(a, E, u0) : 0;
-
+  seg.e = active && warp != 3 ? find_tile(a, E, u0) : 0;
   if (warp == 0) {
     // ---------------- TMA producer: lane i takes the block's i-th page
     const int np = CT_KB >> a.c.ps_log2, ps = 1 << a.c.ps_log2;
     const int gone = a.c.n_pages * a.c.n_kv * ps;      // past the last row: reads zeros
     int cnt = 0, nseg = 0;
     bool go = true;                                    // the same in every lane
-    for (long long u = u0; u < u1 && go; u += seg.nv) {
+    for (int u = u0; u < u1 && go; u += seg.nv) {
       seg.at(a, u, u1);
       if (seg.n == 0) break;                            // the run ends in a tile's overhead
       // the tile's queries: G heads of a.rt / G rows, in packed order
@@ -194,7 +190,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                    dv = desc_sw128_mn(smem_u32(sKV), C::BOX);
     int cnt = 0, nseg = 0;                              // ring entries of earlier segments
     uint32_t pc0 = 0, pc1 = 0;
-    for (long long u = u0; u < u1; u += seg.nv, ++nseg) {
+    for (int u = u0; u < u1; u += seg.nv, ++nseg) {
       seg.at(a, u, u1);
       if (seg.n == 0) break;
       const int n = __shfl_sync(0xffffffffu, seg.n, 0);
@@ -238,6 +234,15 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
       cnt += 2 * n;
       seg.done(a);
     }
+  } else if (warp == 2) {
+    // ---------------- what the join kernel finds at this run's start
+    if (lane == 0 && !active) a.plan_join[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (lane == 0 && active) {
+      seg.at(a, u0, u1);
+      const int t0 = a.plan_first[seg.e] * a.c.n_kv;
+      put_join(a, w, blockIdx.x, t0 + seg.g * (seg.nb + a.ov), seg.nb + a.ov, seg.row0, seg.g, seg.x0,
+               seg.all);
+    }
   } else if (warp >= 4) {
     // ---------------- softmax: thread = packed row `r` of pair `p`
     const int p = (warp - 4) >> 2, r = tid & 127;
@@ -248,7 +253,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     int cnt = 0;                                        // ring entries of earlier segments
     const int np = CT_KB >> a.c.ps_log2;
     const uint32_t all_pages = (1u << np) - 1u;
-    for (long long u = u0; u < u1; u += seg.nv) {
+    for (int u = u0; u < u1; u += seg.nv) {
       seg.at(a, u, u1);
       if (seg.n == 0) break;
       const SeenBlocks<CT_KB> blocks(seg.seen);
