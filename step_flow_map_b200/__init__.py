@@ -156,9 +156,7 @@ def _ptr(x):
 
 
 def _stream(s):
-    if s is None:
-        return None
-    if isinstance(s, int):
+    if s is None or isinstance(s, int):
         return s
     return s.cuda_stream
 

@@ -6,6 +6,8 @@ runs here.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -102,6 +104,9 @@ class Context:
         return n, br, out
 
 
+_HERE = contextlib.nullcontext()   # the current device and stream serve as they are
+
+
 class PagedCache:
     """One layer of the target's paged key/value cache: torch tensors in the
     library's layout, and the operators that work on them (argument checks and
@@ -124,7 +129,10 @@ class PagedCache:
             raise ValueError("k must be [n_pages, n_kv_heads, page_size, head_dim], bf16 or fp32")
         self.k, self.v, self.pos, self.weight = k, v, pos, weight
         self.device = k.device
+        self._ws_bytes = {}
         n_pages, n_kv, ps, dh = k.shape
+        if k.is_cuda and k.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self._check("v", v, k.dtype, k.shape)
         for name, t, dt in (("pos", pos, torch.int32), ("weight", weight, torch.float32)):
             if t is not None:
@@ -151,21 +159,21 @@ class PagedCache:
         self._c.page_table, self._c.table_stride = t.data_ptr(), t.shape[1]
 
     def _check(self, name, t, dtype, shape):
-        if t.device != self.device or t.dtype != dtype or tuple(t.shape) != tuple(shape) \
-                or not t.is_contiguous():
+        if t.shape != shape or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
                              f"on {self.device}")
 
-    def _rows(self, name, t, heads):
+    def _rows(self, name, t, T, heads):
         """Row stride of a [T, heads, head_dim] tensor whose heads are contiguous."""
         dh = self._c.head_dim
-        if t.dim() != 3 or t.shape[2] != dh or (heads and t.shape[1] != heads) \
-                or t.dtype != self.k.dtype or t.device != self.device \
-                or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dh))):
-            raise ValueError(f"{name} must be [T, heads, {dh}] {self.k.dtype} on {self.device} "
-                             "with contiguous heads")
+        if t.shape != (T, heads, dh) or t.dtype != self.k.dtype or t.device != self.device:
+            raise ValueError(f"{name} must be [{T}, {heads}, {dh}] {self.k.dtype} on {self.device}")
+        st = t.stride()
+        if st[2] != 1 or (heads > 1 and st[1] != dh):
+            if t.numel():
+                raise ValueError(f"{name} must have contiguous heads")
         # one row's stride says nothing; any aligned one will do
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dh
+        return st[0] if T > 1 else heads * dh
 
     def _seqs(self, T, cu_rows, kv_len, q_pos):
         B = kv_len.shape[0]
@@ -178,22 +186,25 @@ class PagedCache:
         return B
 
     def _on(self, stream):
-        """(context that makes `stream` current on the cache's device, the stream)."""
-        if stream is None:
-            with torch.cuda.device(self.device):
-                stream = torch.cuda.current_stream()
-        elif isinstance(stream, int):
+        """A context under which tensors are allocated on the cache's device and on
+        `stream` (None: the device's current stream), and that stream."""
+        if stream is None:   # (the public accessors cost 5 us, as much as a small call's kernels)
+            dev = self.device.index
+            st = torch._C._cuda_getCurrentRawStream(dev)
+            return (_HERE if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)), st
+        if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
-        return torch.cuda.stream(stream), stream
+        return torch.cuda.stream(stream), stream.cuda_stream
 
     def append(self, q, k, v, cu_rows, kv_len, q_pos=None, *, q_gain=None, k_gain=None, eps=1e-6,
                inv_freq=None, interleaved=False, out=None, stream=None):
         """Norms, rotates and appends the new rows; returns the queries [T, n_heads, head_dim]."""
         n_kv, dh = self._c.n_kv_heads, self._c.head_dim
+        if q.dim() != 3:
+            raise ValueError("q must be [T, n_heads, head_dim]")
         T, n_heads = q.shape[0], q.shape[1]
-        qs, ks, vs = self._rows("q", q, 0), self._rows("k", k, n_kv), self._rows("v", v, n_kv)
-        if k.shape[0] != T or v.shape[0] != T:
-            raise ValueError("q, k and v must have the same rows")
+        qs = self._rows("q", q, T, n_heads)
+        ks, vs = self._rows("k", k, T, n_kv), self._rows("v", v, T, n_kv)
         B = self._seqs(T, cu_rows, kv_len, q_pos)
         for name, g in (("q_gain", q_gain), ("k_gain", k_gain)):
             if g is not None:
@@ -206,41 +217,43 @@ class PagedCache:
         with ctx:
             if out is None:
                 out = torch.empty((T, n_heads, dh), dtype=q.dtype, device=self.device)
-            elif out.shape != q.shape:
-                raise ValueError("out must have q's shape")
+            os = self._rows("out", out, T, n_heads)
+            # positional, in the structure's order
             fm_cache_append(self._c, fm_append_args(
-                T=T, B=B, n_heads=n_heads, q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(),
-                q_stride=qs, k_stride=ks, v_stride=vs,
-                q_gain=q_gain.data_ptr() if q_gain is not None else None,
-                k_gain=k_gain.data_ptr() if k_gain is not None else None, eps=eps,
-                inv_freq=inv_freq.data_ptr() if rot else None, rot_dim=rot,
-                interleaved=int(bool(interleaved)), cu_rows=cu_rows.data_ptr(),
-                kv_len=kv_len.data_ptr(), q_pos=q_pos.data_ptr() if q_pos is not None else None,
-                q_out=out.data_ptr(), q_out_stride=self._rows("out", out, n_heads)), st)
+                T, B, n_heads, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+                None if q_gain is None else q_gain.data_ptr(),
+                None if k_gain is None else k_gain.data_ptr(), eps,
+                inv_freq.data_ptr() if rot else None, rot, int(bool(interleaved)),
+                cu_rows.data_ptr(), kv_len.data_ptr(),
+                None if q_pos is None else q_pos.data_ptr(), out.data_ptr(), os), st)
         return out
 
     def attend(self, q, cu_rows, kv_len, *, max_rows, max_kv, q_pos=None, scale=None, window=0,
                sinks=0, accumulate=False, lse=False, out=None, stream=None):
         """Attention of the new rows; returns out, or (out, lse) with ``lse=True``."""
-        T, n_heads = q.shape[0], q.shape[1]
-        qs = self._rows("q", q, 0)
+        if q.dim() != 3:
+            raise ValueError("q must be [T, n_heads, head_dim]")
+        T, n_heads, dh = q.shape
+        qs = self._rows("q", q, T, n_heads)
         B = self._seqs(T, cu_rows, kv_len, q_pos)
         ctx, st = self._on(stream)
         with ctx:
             if out is None:
-                out = torch.empty((T, n_heads, q.shape[2]), dtype=q.dtype, device=self.device)
-            elif out.shape != q.shape:
-                raise ValueError("out must have q's shape")
+                out = torch.empty((T, n_heads, dh), dtype=q.dtype, device=self.device)
+            os = self._rows("out", out, T, n_heads)
             got = torch.empty((T, n_heads), dtype=torch.float32, device=self.device) if lse else None
             a = fm_attention_args(
-                T=T, B=B, n_heads=n_heads, max_rows=max_rows, max_kv=max_kv, q=q.data_ptr(),
-                q_stride=qs, cu_rows=cu_rows.data_ptr(), kv_len=kv_len.data_ptr(),
-                q_pos=q_pos.data_ptr() if q_pos is not None else None,
-                scale=scale if scale is not None else q.shape[2] ** -0.5, window=window, sinks=sinks,
-                accumulate=int(bool(accumulate)), out=out.data_ptr(),
-                out_stride=self._rows("out", out, n_heads),
-                lse=got.data_ptr() if lse else None)
-            ws_bytes = fm_cache_attention_workspace(self._c, a)
+                T, B, n_heads, max_rows, max_kv, q.data_ptr(), qs, cu_rows.data_ptr(),
+                kv_len.data_ptr(), None if q_pos is None else q_pos.data_ptr(),
+                dh ** -0.5 if scale is None else scale, window, sinks, int(bool(accumulate)),
+                out.data_ptr(), os, got.data_ptr() if lse else None)
+            # a function of the sizes alone
+            key = (T, B, n_heads, max_rows, max_kv, a.accumulate)
+            ws_bytes = self._ws_bytes.get(key)
+            if ws_bytes is None:
+                if len(self._ws_bytes) > 256:
+                    self._ws_bytes.clear()
+                ws_bytes = self._ws_bytes[key] = fm_cache_attention_workspace(self._c, a)
             ws = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device)
             fm_cache_attention(self._c, a, ws, ws_bytes, st)
         return (out, got) if lse else out
@@ -256,8 +269,9 @@ class PagedCache:
         ctx, st = self._on(stream)
         with ctx:
             if new_len is None:
-                new_len = torch.empty_like(kv_len)
+                new_len = torch.empty((B,), dtype=torch.int32, device=self.device)
             else:
                 self._check("new_len", new_len, torch.int32, (B,))
-            fm_cache_evict(self._c, kv_len, next_pos, B, max_kv, budget, sinks, recent, new_len, st)
+            fm_cache_evict(self._c, kv_len.data_ptr(), next_pos.data_ptr(), B, max_kv, budget, sinks,
+                           recent, new_len.data_ptr(), st)
         return new_len
