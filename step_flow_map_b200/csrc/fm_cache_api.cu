@@ -12,6 +12,7 @@
 #include "fm_cache_attn.cuh"
 #include "fm_cache_decode.cuh"
 #include "fm_cache_tc.cuh"
+#include "fm_cache_weights.cuh"
 
 using fm::bf16;
 
@@ -183,7 +184,8 @@ struct AttnPlan {
   enum { DECODE, TC_ONE, TC_PAIR, SIMT } kind = SIMT;
   int qt = 0, rt = 0, tile_rows = 0, ov = 0, grid = 0;   // rows of a partial; see CacheAttnArgs
   int64_t tiles = 0;
-  size_t o_first = 0, o_tile = 0, o_join = 0, o_lse = 0, o_ml = 0, o_part = 0, total = 0;
+  bool keep = false;
+  size_t o_first = 0, o_tile = 0, o_join = 0, o_lse = 0, o_scores = 0, o_ml = 0, o_part = 0, total = 0;
 };
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -235,6 +237,11 @@ fm_status plan_attention(const fm_paged_cache* c, const fm_attention_args* a, At
   at = up256(at + (size_t)p->grid * 2 * sizeof(int4));
   p->o_lse = at;
   if (a->accumulate) at = up256(at + (size_t)a->T * a->n_heads * sizeof(float));
+  // scores of few packed rows are kept for the weights (see score_at)
+  p->keep = a->accumulate && rows <= 16;
+  p->o_scores = at;
+  if (p->keep)
+    at = up256(at + (size_t)a->B * c->n_kv_heads * ((a->max_kv + 15) / 16) * rows * 64);
   p->o_ml = at;
   at = up256(at + (size_t)p->grid * 2 * p->qt * sizeof(float2));
   p->o_part = at;
@@ -329,12 +336,22 @@ fm_status run_attention(const fm::CacheAttnArgs& k, const AttnPlan& p, int accum
     else FM_TRY((launch_tc<DH, true>(k, p, st)));
   } else if (p.qt == 16) FM_TRY((launch_simt<T, DH, 16>(k, p, st)));
   else FM_TRY((launch_simt<T, DH, 64>(k, p, st)));
-  if (accumulate) {
-    const int per = fm::CW_THREADS / 32;
-    const int gx = std::max(1, std::min((k.max_kv + per - 1) / per, 64));
-    FM_LAUNCH_OK("cache weights",
-                 fm::launch_pdl(fm::k_cache_weights<T, DH>, dim3(gx, k.c.n_kv, k.B),
-                                dim3(fm::CW_THREADS), 0, st, k));
+  if (!accumulate) return FM_OK;
+  // at least two waves of CTAs where the rows allow it
+  auto grid = [&](int per) {
+    return dim3((unsigned)std::max(1, std::min((k.max_kv + per - 1) / per, 256)), k.c.n_kv, k.B);
+  };
+  if (k.scores) {
+    FM_LAUNCH_OK("cache weights", fm::launch_pdl(fm::k_cache_weights_scores, grid(fm::CW_THREADS),
+                                                 dim3(fm::CW_THREADS), 0, st, k));
+  } else if constexpr (std::is_same<T, bf16>::value) {
+    auto kernel = fm::k_cache_weights_mma<DH>;
+    FM_CUDA(fm::set_smem_once(kernel, fm::WmCfg<DH>::SMEM));
+    FM_LAUNCH_OK("cache weights", fm::launch_pdl(kernel, grid(fm::WM_KEYS), dim3(fm::WM_THREADS),
+                                                 fm::WmCfg<DH>::SMEM, st, k));
+  } else {
+    FM_LAUNCH_OK("cache weights", fm::launch_pdl(fm::k_cache_weights<T, DH>, grid(fm::CW_THREADS / 32),
+                                                 dim3(fm::CW_THREADS), 0, st, k));
   }
   return FM_OK;
 }
@@ -395,6 +412,7 @@ extern "C" fm_status fm_cache_attention(const fm_paged_cache* c, const fm_attent
   k.plan_join = (int4*)(w + p.o_join);
   k.part_ml = (float2*)(w + p.o_ml);
   k.part = (float*)(w + p.o_part);
+  k.scores = p.keep ? (float*)(w + p.o_scores) : nullptr;
   cudaStream_t st = (cudaStream_t)stream;
   if (c->dtype == FM_BF16)
     return c->head_dim == 128 ? run_attention<bf16, 128>(k, p, a->accumulate, st)

@@ -39,6 +39,7 @@ struct CacheAttnArgs {
   int4* plan_join;                 // [grid][2], see JoinItem
   float* part;                     // [grid][2][QT][DH]
   float2* part_ml;                 // [grid][2][QT]: (max, sum), log2 units
+  float* scores;                   // see score_at, or null
 };
 
 // Rows a tile can see: [0, s_end) and [lo, hi), s_end <= lo.
@@ -80,6 +81,13 @@ __device__ __forceinline__ bool row_seen(const SeenRows& s, int r) {
 // taken unsigned once the order is known, so no pair of positions overflows.
 __device__ __forceinline__ bool sees(int pq, int pk, int window, int sinks) {
   return pk <= pq && (window == 0 || (unsigned)pq - (unsigned)pk < (unsigned)window || pk < sinks);
+}
+
+// Masked scores (log2 units) of the cache row r of (b, g) against packed row x
+// of at most a.max_rows G <= 16, 16 neighbouring cache rows side by side.
+__device__ __forceinline__ size_t score_at(const CacheAttnArgs& a, int b, int g, int r, int x) {
+  const size_t tiles = (size_t)((a.max_kv + 15) >> 4);
+  return ((((size_t)b * a.c.n_kv + g) * tiles + (r >> 4)) * (a.max_rows * a.G) + x) * 16 + (r & 15);
 }
 
 // ------------------------------------------------------------------ plan
@@ -332,6 +340,8 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
         for (int k = 0; k < C::KPT; ++k) {
           const int kr = tc + C::TC * k;
           if (!(s_ok[kr] && sees(pq[i], s_pos[kr], a.window, a.sinks))) sc[i][k] = -INFINITY;
+          if (QT == 16 && a.scores && tr + C::TR * i < rows && row_seen(seen, r0 + kr))
+            a.scores[score_at(a, b, g, r0 + kr, tr + C::TR * i)] = sc[i][k];
           mx = fmaxf(mx, sc[i][k]);
         }
 #pragma unroll
@@ -495,15 +505,49 @@ __global__ void __launch_bounds__(CJ_THREADS) k_cache_join_cols(const CacheAttnA
 }
 
 // ------------------------------------------------------------------ weights
-// weight_r += sum over queries and heads of e^(s - lse): one warp per cache
-// row, the key in registers, the queries in order (no atomics, so the sum
-// does not depend on scheduling).
+// weight_r += sum over queries and heads of e^(s - lse), added up in the order
+// of the packed rows (no atomics, so the sum does not depend on scheduling).
+
+// Few packed rows: from the scores the attention kernel left, a thread per
+// cache row.  Bound: HBM, 4 bytes per score and 8 per weight -- for four query
+// heads per key/value head 24 bytes a row against the 256 that reading the
+// keys again would take.
 constexpr int CW_THREADS = 256;
-template <typename T, int DH>
-__global__ void __launch_bounds__(CW_THREADS) k_cache_weights(const CacheAttnArgs a) {
+__global__ void __launch_bounds__(CW_THREADS) k_cache_weights_scores(const CacheAttnArgs a) {
+  __shared__ float s_lse[16];
+  const int g = blockIdx.y, b = blockIdx.z;
   pdl_wait();
   pdl_trigger();
+  const NewRows s = new_rows(a.cu, a.kv_len, b, a.T);
+  const int n = min(s.n, a.max_rows), rows = n * a.G;
+  if (n == 0) return;
+  if (threadIdx.x < rows) {
+    const int x = threadIdx.x;
+    const float v = a.lse[(size_t)(s.first + x / a.G) * a.n_heads + g * a.G + x % a.G];
+    s_lse[x] = v == -INFINITY ? INFINITY : v * 1.4426950408889634f;   // 2^(s - inf) = 0
+  }
+  __syncthreads();
+  const SeenRows seen = seen_rows(a, s, 0, n - 1);
+  for (int r = blockIdx.x * CW_THREADS + threadIdx.x; r < seen.hi; r += gridDim.x * CW_THREADS) {
+    const int page = row_seen(seen, r) ? cache_page(a.c, b, r) : -1;
+    if (page < 0) continue;
+    float* w = a.c.weight + cache_row(a.c, page, g, r);
+    const float had = *w;
+    const float* p = a.scores + score_at(a, b, g, r, 0);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int x = 0; x < rows; ++x) sum += exp2f(p[x * 16] - s_lse[x]);
+    *w = had + sum;
+  }
+}
+
+// Many packed rows, fp32: one warp per cache row, the key in registers, the
+// scores once more.
+template <typename T, int DH>
+__global__ void __launch_bounds__(CW_THREADS) k_cache_weights(const CacheAttnArgs a) {
   const int lane = threadIdx.x & 31, g = blockIdx.y, b = blockIdx.z;
+  pdl_wait();
+  pdl_trigger();
   const NewRows s = new_rows(a.cu, a.kv_len, b, a.T);
   const int n = min(s.n, a.max_rows);
   if (n == 0) return;

@@ -105,12 +105,6 @@ struct CdCfg {
   static constexpr int SMEM = 4 * RING + 4 * 4 * MLD * 4;
 };
 
-// 16 bytes global -> shared, zeros when `live` is false.
-__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(live ? 16u : 0u)
-               : "memory");
-}
 template <int DH>
 __global__ void __launch_bounds__(CD_THREADS, 2) k_cache_decode(const CacheAttnArgs a) {
   using C = CdCfg<DH>;
@@ -256,6 +250,15 @@ __global__ void __launch_bounds__(CD_THREADS, 2) k_cache_decode(const CacheAttnA
             sc[n][e] = v;
             mx[e >> 1] = fmaxf(mx[e >> 1], v);
           }
+        if (a.scores) {            // kept for the weights: 2 keys, 8 bytes, a thread and row
+          float* dst = a.scores + score_at(a, b, g, r0, 0) + 2 * t4;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (gr + 8 * h < rows)
+#pragma unroll
+              for (int n = 0; n < 2; ++n)
+                *(float2*)(dst + (gr + 8 * h) * 16 + n * 8) = make_float2(sc[n][2 * h], sc[n][2 * h + 1]);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
