@@ -53,9 +53,18 @@ __device__ __forceinline__ NewRows new_rows(const int* cu, const int* kv_len, in
 // Bound: HBM (every value read once and written once) for many rows, launch
 // and one chain of dependent loads for few.  A thread holds 16 bytes of one
 // head, head_dim * size / 16 neighbouring lanes hold the head, so the norm is
-// a few shuffles and a half-split pair one shuffle; a CTA takes whole rows,
-// whose angles (one fp64 product and reduction per pair, shared by all heads)
-// wait in shared memory while the heads' loads are in flight.
+// a few shuffles and a half-split pair one shuffle.  A CTA takes `tok` rows:
+// its warps find the rows' sequences, pages and angles side by side (one fp64
+// product and reduction per pair) while the first row's values are already
+// loading, and leave for every value of a head the cosine and the signed sine
+// of its term, in the order the threads read them; a row's angles then sit in
+// registers for all its heads.  Each row is loaded while the row before it is
+// worked on.  (Angles looked up by pair at each use
+// took 108 us for 12,709 rows of 48 heads of width 128 in bf16; this takes 69,
+// 4.5 TB/s.  At 80 registers three CTAs fit an SM; four at 64 took 80 us, two
+// at 96 85.)  tok is 1 while rows are
+// fewer than four per SM and grows to 8, so that the chain at a CTA's start is
+// paid once per 8 rows.
 constexpr int CA_THREADS = 256;
 constexpr int CA_MAX_TOK = 8;     // rows of one CTA
 constexpr int CA_UNROLL = 3;      // 16-byte loads in flight per thread
@@ -101,38 +110,54 @@ template <> struct Vec16<float> {
   }
 };
 
-template <typename T, int DH>
-__global__ void __launch_bounds__(CA_THREADS) k_cache_append(const AppendArgs a) {
+template <typename T, int DH, bool INTER>
+__global__ void __launch_bounds__(CA_THREADS, 3) k_cache_append(const AppendArgs a) {
   constexpr int VE = Vec16<T>::N, LPH = DH / VE;   // values per thread, lanes per head
-  __shared__ float2 s_cs[CA_MAX_TOK][DH / 2];      // (cos, sin) per row and pair
+  constexpr int STEP = CA_THREADS / LPH;           // heads the CTA covers at once
+  constexpr int PAIRS = (DH / 2 + 31) / 32;
+  // (cosine, signed sine) of value c of a head at [c % VE][c / VE]
+  __shared__ float2 s_cs[CA_MAX_TOK][VE][LPH];
   __shared__ int s_page[CA_MAX_TOK], s_row[CA_MAX_TOK], s_pos[CA_MAX_TOK];
   const int t0 = blockIdx.x * a.tok, nt = min(a.tok, a.T - t0);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int heads = a.n_heads + 2 * a.c.n_kv;
-  const int sub = tid & (LPH - 1), tasks = nt * heads;
-  constexpr int STEP = CA_THREADS / LPH;
+  const int sub = tid & (LPH - 1);
   pdl_wait();
   pdl_trigger();
 
-  auto src = [&](int task) -> const T* {
-    const int t = t0 + task / heads;
-    int h = task % heads;
-    if (h < a.n_heads) return (const T*)a.q + t * a.qs + h * DH;
-    h -= a.n_heads;
-    if (h < a.c.n_kv) return (const T*)a.k + t * a.ks + h * DH;
-    return (const T*)a.v + t * a.vs + (h - a.c.n_kv) * DH;
+  // rows side by side when their heads are fewer than STEP; this thread's
+  // first row and head
+  const int side = max(1, STEP / heads), slot = tid / LPH;
+  const int j0 = side == 1 ? 0 : slot / heads, h0 = side == 1 ? slot : slot - j0 * heads;
+  const int j_end = j0 < side ? nt : 0;
+  // heads are numbered q, k, v; the k and v row pointers stand so far back
+  // that head h of any kind lies h DH values on
+  const int k_at = a.n_heads, v_at = a.n_heads + a.c.n_kv;
+  const T *pq = (const T*)a.q + (t0 + j0) * a.qs + sub * VE,
+          *pk = (const T*)a.k + (t0 + j0) * a.ks + sub * VE - k_at * DH,
+          *pv = (const T*)a.v + (t0 + j0) * a.vs + sub * VE - v_at * DH;
+  auto load = [&](int h) -> uint4 {
+    return *(const uint4*)((h < k_at ? pq : h < v_at ? pk : pv) + h * DH);
   };
-  // the first heads' loads go out before anything else
   uint4 x[CA_UNROLL];
 #pragma unroll
-  for (int u = 0; u < CA_UNROLL; ++u) {
-    const int task = tid / LPH + u * STEP;
-    if (task < tasks) x[u] = *((const uint4*)src(task) + sub);
-  }
+  for (int u = 0; u < CA_UNROLL; ++u)
+    if (j0 < j_end && h0 + u * STEP < heads) x[u] = load(h0 + u * STEP);
+  uint4 gq = make_uint4(0, 0, 0, 0), gk = gq;
+  if (a.qg) gq = __ldg((const uint4*)a.qg + sub);
+  if (a.kg) gk = __ldg((const uint4*)a.kg + sub);
+
   // a warp per row: its sequence (all of cu_rows and kv_len in one round of
-  // loads), page and position
+  // loads), page and angles
   for (int j = warp; j < nt; j += CA_THREADS / 32) {
     const int t = t0 + j;
+    const int given = a.q_pos ? __ldg(a.q_pos + t) : 0;
+    double f[PAIRS];
+#pragma unroll
+    for (int k = 0; k < PAIRS; ++k) {
+      const int i = lane + 32 * k;
+      f[k] = i < a.rot / 2 ? a.inv_freq[i] : 0.0;
+    }
     int row = -1, seq = -1;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
@@ -149,100 +174,109 @@ __global__ void __launch_bounds__(CA_THREADS) k_cache_append(const AppendArgs a)
       row = __shfl_sync(0xffffffffu, row, __ffs((int)hit) - 1);
       seq = __shfl_sync(0xffffffffu, seq, __ffs((int)hit) - 1);
     }
+    const int p = a.q_pos ? given : row;
     if (lane == 0) {
-      const int p = a.q_pos ? __ldg(a.q_pos + t) : row;
       s_pos[j] = p;
       s_row[j] = row;
       s_page[j] = hit ? cache_page(a.c, seq, row) : -2;   // -2: a row of no sequence
     }
-    const int p = __shfl_sync(0xffffffffu, lane == 0 ? s_pos[j] : 0, 0);
     // turns = position * f / (2 pi): its whole part drops out in fp64, so the
     // fraction is good to 1e-10 of a turn at any 32-bit position
-    for (int i = lane; i < a.rot / 2; i += 32) {
-      const double turns = (double)p * a.inv_freq[i] * 0.15915494309189533577;
-      float c, s;
-      sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-      s_cs[j][i] = make_float2(c, s);
+#pragma unroll
+    for (int k = 0; k < PAIRS; ++k) {
+      const int i = lane + 32 * k;
+      if (i < a.rot / 2) {
+        const double turns = (double)p * f[k] * 0.15915494309189533577;
+        float c, s;
+        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+        const int lo = INTER ? 2 * i : i, hi = INTER ? 2 * i + 1 : i + a.rot / 2;
+        s_cs[j][lo % VE][lo / VE] = make_float2(c, -s);
+        s_cs[j][hi % VE][hi / VE] = make_float2(c, s);
+      }
     }
+    for (int c = a.rot + lane; c < DH; c += 32) s_cs[j][c % VE][c / VE] = make_float2(1.f, 0.f);
   }
   __syncthreads();
 
+  if (a.c.pos || a.c.weight)
+    for (int i = tid; i < nt * a.c.n_kv; i += CA_THREADS) {
+      const int j = i / a.c.n_kv, g = i - j * a.c.n_kv;
+      if (s_page[j] < 0) continue;
+      const size_t at = cache_row(a.c, s_page[j], g, s_row[j]);
+      if (a.c.pos) a.c.pos[at] = s_pos[j];
+      if (a.c.weight) a.c.weight[at] = 0.f;
+    }
+
   // shuffles stay among a head's lanes, which always branch together
   const unsigned m = LPH == 32 ? 0xffffffffu : ((1u << (LPH & 31)) - 1u) << (lane & ~(LPH - 1));
-  for (int task0 = 0; task0 < tasks; task0 += STEP * CA_UNROLL) {
-    if (task0 > 0) {
+  // half-split pairs: a thread's values pair with those rot/2 on (or back), a
+  // whole number of lanes away (rot is a multiple of 16)
+  const int c0 = sub * VE, far = (a.rot >> 1) / VE;
+  const int peer = (lane & ~(LPH - 1)) +
+                   (c0 >= a.rot ? sub : c0 < (a.rot >> 1) ? sub + far : sub - far);
+  for (int j = j0; j < j_end; j += side) {
+    float cs[VE], sn[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float2 v = s_cs[j][e][sub];
+      cs[e] = v.x;
+      sn[e] = v.y;
+    }
+    // where head h's result goes: + h DH (queries), + h page rows (keys, values)
+    const int page = s_page[j];
+    const size_t at0 = cache_row(a.c, max(page, 0), 0, s_row[j]);
+    T* const dq = (T*)a.q_out + (t0 + j) * a.os + sub * VE;
+    T* const dk = (T*)a.c.k + (at0 - ((size_t)k_at << a.c.ps_log2)) * DH + sub * VE;
+    T* const dv = (T*)a.c.v + (at0 - ((size_t)v_at << a.c.ps_log2)) * DH + sub * VE;
+    for (int hb = h0; hb < heads; hb += STEP * CA_UNROLL) {
+      // the next group: further heads of this row, or the next row
+      uint4 y[CA_UNROLL];
+      int nh = hb + STEP * CA_UNROLL;
+      if (nh >= heads) {
+        nh = j + side < j_end ? h0 : heads;
+        pq += side * a.qs;
+        pk += side * a.ks;
+        pv += side * a.vs;
+      }
+#pragma unroll
+      for (int u = 0; u < CA_UNROLL; ++u)
+        if (nh + u * STEP < heads) y[u] = load(nh + u * STEP);
 #pragma unroll
       for (int u = 0; u < CA_UNROLL; ++u) {
-        const int task = task0 + tid / LPH + u * STEP;
-        if (task < tasks) x[u] = *((const uint4*)src(task) + sub);
-      }
-    }
+        const int h = hb + u * STEP;
+        if (h >= heads) break;
+        const bool is_q = h < k_at;
+        uint4 out = x[u];
+        if (h < v_at) {
+          float f[VE], r = 1.f;
+          Vec16<T>::unpack(x[u], f);
+          if (is_q ? a.qg != nullptr : a.kg != nullptr) {
+            float ss = 0.f;
 #pragma unroll
-    for (int u = 0; u < CA_UNROLL; ++u) {
-      const int task = task0 + tid / LPH + u * STEP;
-      if (task >= tasks) continue;
-      const int j = task / heads, t = t0 + j;
-      int h = task % heads;
-      const int page = s_page[j];
-      if (h >= a.n_heads + a.c.n_kv) {
-        h -= a.n_heads + a.c.n_kv;
-        if (page >= 0)
-          *((uint4*)((T*)a.c.v + cache_row(a.c, page, h, s_row[j]) * DH) + sub) = x[u];
-        continue;
-      }
-      const bool is_q = h < a.n_heads;
-      if (!is_q) h -= a.n_heads;
-      float f[VE];
-      Vec16<T>::unpack(x[u], f);
-      const T* gain = (const T*)(is_q ? a.qg : a.kg);
-      if (gain) {
-        float ss = 0.f;
+            for (int e = 0; e < VE; ++e) ss = fmaf(f[e], f[e], ss);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) ss = fmaf(f[e], f[e], ss);
+            for (int z = LPH / 2; z > 0; z >>= 1) ss += __shfl_xor_sync(m, ss, z);
+            r = rsqrtf(ss * (1.f / DH) + a.eps);
+            float g[VE];
+            Vec16<T>::unpack(is_q ? gq : gk, g);
 #pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(m, ss, o);
-        const float r = rsqrtf(ss * (1.f / DH) + a.eps);
-        float gv[VE];
-        Vec16<T>::unpack(__ldg((const uint4*)gain + sub), gv);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) f[e] *= r * gv[e];
-      }
-      const int c0 = sub * VE;   // this thread's first value of the head
-      if (a.interleaved) {
-        if (c0 < a.rot) {
-#pragma unroll
-          for (int e = 0; e < VE; e += 2) {
-            const float2 cs = s_cs[j][(c0 + e) >> 1];
-            const float lo = f[e], hi = f[e + 1];
-            f[e] = lo * cs.x - hi * cs.y;
-            f[e + 1] = hi * cs.x + lo * cs.y;
+            for (int e = 0; e < VE; ++e) f[e] *= g[e];
           }
-        }
-      } else if (a.rot > 0) {
-        // the partner of values c0.. lies rot/2 values on (or back), a whole
-        // number of lanes away (rot is a multiple of 16)
-        const int half = a.rot >> 1, d = half / VE;
-        const bool low = c0 < half, in = c0 < a.rot;
-        const int peer = (lane & ~(LPH - 1)) + (!in ? sub : low ? sub + d : sub - d);
+          float o[VE];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const float o = __shfl_sync(m, f[e], peer);
-          if (in) {
-            const float2 cs = s_cs[j][(low ? c0 : c0 - half) + e];
-            f[e] = low ? f[e] * cs.x - o * cs.y : f[e] * cs.x + o * cs.y;
-          }
+          for (int e = 0; e < VE; ++e) o[e] = INTER ? f[e ^ 1] : __shfl_sync(m, f[e], peer);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) f[e] = r * fmaf(o[e], sn[e], f[e] * cs[e]);
+          out = Vec16<T>::pack(f);
+        }
+        if (is_q) {
+          if (page != -2) *(uint4*)(dq + h * DH) = out;
+        } else if (page >= 0) {
+          *(uint4*)((h < v_at ? dk : dv) + ((size_t)h << a.c.ps_log2) * DH) = out;
         }
       }
-      if (is_q) {
-        if (page != -2) *((uint4*)((T*)a.q_out + t * a.os + h * DH) + sub) = Vec16<T>::pack(f);
-      } else if (page >= 0) {
-        const size_t at = cache_row(a.c, page, h, s_row[j]);
-        *((uint4*)((T*)a.c.k + at * DH) + sub) = Vec16<T>::pack(f);
-        if (sub == 0) {
-          if (a.c.pos) a.c.pos[at] = s_pos[j];
-          if (a.c.weight) a.c.weight[at] = 0.f;
-        }
-      }
+#pragma unroll
+      for (int u = 0; u < CA_UNROLL; ++u) x[u] = y[u];
     }
   }
 }
@@ -433,36 +467,51 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const EvictArgs a) {
   // L - budget) <= L / 2 entries, so two lists fit the key array.
   const uint32_t lists = (uint32_t)__cvta_generic_to_shared(key);
   const uint32_t half = (uint32_t)(a.slice_cap / 2) * 4u;
+  // the entries are row indices of the whole cache (31 bits; all ones: the row
+  // does not exist), looked up here, where every thread has its own
   for (int i = i0; i < i1; ++i) {
-    const bool in = (keep >> (i - i0)) & 1ull;
-    if (r0 + i < a.budget) {
-      if (!in) {
-        dsmem_stu(dsmem_addr(lists, hole % C) + (hole / C) * 4u, (unsigned)(r0 + i));
-        ++hole;
-      }
-    } else if (in) {
-      dsmem_stu(dsmem_addr(lists + half, mover % C) + (mover / C) * 4u, (unsigned)(r0 + i));
-      ++mover;
-    }
+    const bool in = (keep >> (i - i0)) & 1ull, low = r0 + i < a.budget;
+    if (in == low) continue;
+    const int page = cache_page(a.c, b, r0 + i);
+    const unsigned at = page < 0 ? 0xffffffffu : (unsigned)cache_row(a.c, page, g, r0 + i);
+    const unsigned e = low ? hole++ : mover++;
+    dsmem_stu(dsmem_addr(low ? lists : lists + half, e % C) + (e / C) * 4u, at);
   }
   cluster_sync_all();
   const int mine = ((int)moves - z + C - 1) / C;
   const uint32_t* to_row = key;
   const uint32_t* from_row = key + a.slice_cap / 2;
   const int per = a.row_bytes >> 4;                 // 16-byte pieces of a row: 4 .. 32
-  for (int e = warp; e < mine; e += EV_THREADS / 32) {
-    const int dr = (int)to_row[e], sr = (int)from_row[e];
-    const int dp = cache_page(a.c, b, dr), sp = cache_page(a.c, b, sr);
-    if (dp < 0 || sp < 0) continue;
-    const size_t d = cache_row(a.c, dp, g, dr), s = cache_row(a.c, sp, g, sr);
-    for (int i = lane; i < 2 * per; i += 32) {
-      const bool val = i >= per;
-      const int o = val ? i - per : i;
-      const char* base = (const char*)(val ? a.c.v : a.c.k);
-      *((uint4*)(base + d * a.row_bytes) + o) = *((const uint4*)(base + s * a.row_bytes) + o);
+  // a row's keys and values are 2 per pieces of 16 bytes; a warp moves UN rows
+  // at a time, all loads before the first store
+  constexpr int W = EV_THREADS / 32, UN = 4;
+  for (int e0 = warp; e0 < mine; e0 += W * UN) {
+    size_t d[UN], s[UN];
+    bool ok[UN];
+#pragma unroll
+    for (int k = 0; k < UN; ++k) {
+      const int e = e0 + k * W;
+      const unsigned dr = e < mine ? to_row[e] : ~0u, sr = e < mine ? from_row[e] : ~0u;
+      ok[k] = dr != ~0u && sr != ~0u;
+      d[k] = dr;
+      s[k] = sr;
     }
-    if (lane == 0) a.c.pos[d] = a.c.pos[s];
-    if (lane == 1) a.c.weight[d] = a.c.weight[s];
+    for (int i = lane; i < 2 * per; i += 32) {
+      const int o = i >= per ? i - per : i;
+      char* base = (char*)(i >= per ? a.c.v : a.c.k);
+      uint4 v[UN];
+#pragma unroll
+      for (int k = 0; k < UN; ++k)
+        if (ok[k]) v[k] = *((const uint4*)(base + s[k] * a.row_bytes) + o);
+#pragma unroll
+      for (int k = 0; k < UN; ++k)
+        if (ok[k]) *((uint4*)(base + d[k] * a.row_bytes) + o) = v[k];
+    }
+#pragma unroll
+    for (int k = 0; k < UN; ++k) {
+      if (ok[k] && lane == 2 * k) a.c.pos[d[k]] = a.c.pos[s[k]];
+      if (ok[k] && lane == 2 * k + 1) a.c.weight[d[k]] = a.c.weight[s[k]];
+    }
   }
 }
 

@@ -113,8 +113,9 @@ fm_status device_sms(int* sms) {
 namespace {
 template <typename T, int DH>
 fm_status launch_append(const fm::AppendArgs& a, cudaStream_t st) {
+  auto kernel = a.interleaved ? fm::k_cache_append<T, DH, true> : fm::k_cache_append<T, DH, false>;
   FM_LAUNCH_OK("cache append",
-               fm::launch_pdl(fm::k_cache_append<T, DH>, dim3((unsigned)((a.T + a.tok - 1) / a.tok)),
+               fm::launch_pdl(kernel, dim3((unsigned)((a.T + a.tok - 1) / a.tok)),
                               dim3(fm::CA_THREADS), 0, st, a));
   return FM_OK;
 }
@@ -163,9 +164,9 @@ extern "C" fm_status fm_cache_append(const fm_paged_cache* c, const fm_append_ar
   k.kv_len = a->kv_len;
   k.q_pos = a->q_pos;
   k.q_out = a->q_out;
-  // rows per CTA: as many as its threads hold with CA_UNROLL loads each
-  const int per_row = (a->n_heads + 2 * c->n_kv_heads) * (c->head_dim * esize(c) / 16);
-  k.tok = std::max(1, std::min(fm::CA_MAX_TOK, fm::CA_THREADS * fm::CA_UNROLL / per_row));
+  int sms = 0;
+  FM_TRY(device_sms(&sms));
+  k.tok = std::max(1, std::min(fm::CA_MAX_TOK, a->T / (4 * sms)));
   cudaStream_t st = (cudaStream_t)stream;
   if (c->dtype == FM_BF16)
     return c->head_dim == 128 ? launch_append<bf16, 128>(k, st) : launch_append<bf16, 64>(k, st);
@@ -259,7 +260,7 @@ fm_status launch_simt(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_
   FM_LAUNCH_OK("cache attention", fm::launch_pdl(fm::k_cache_attn_simt<T, DH, QT>, dim3(p.grid),
                                                  dim3(fm::CS_THREADS), C::SMEM, st, k));
   FM_LAUNCH_OK("cache attention join",
-               fm::launch_pdl(fm::k_cache_join_rows<T, DH, QT>, dim3(p.grid - 1, QT),
+               fm::launch_pdl(fm::k_cache_join_rows<T, DH, QT>, dim3(p.grid - 1, (unsigned)std::min<int64_t>(QT, (int64_t)k.max_rows * k.G)),
                               dim3(fm::CJ_THREADS), 0, st, k));
   return FM_OK;
 }
