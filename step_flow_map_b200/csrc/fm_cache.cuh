@@ -286,17 +286,16 @@ __global__ void __launch_bounds__(CA_THREADS, 3) k_cache_append(const AppendArgs
 // [z S, (z + 1) S) of the L rows and keeps its rows' 32-bit sort keys in
 // shared memory, so positions and weights are read once.  Selection: three
 // radix passes (11, 11, 10 bits) of cluster-wide histograms give the budget-th
-// largest key and how many of its ties stay; one ordered scan per thread run
-// gives every hole and every mover its rank; entry i of both lists lives in
+// largest key and how many of its ties stay; ballots and prefix sums give every
+// hole and every mover its rank; entry i of both lists lives in
 // CTA i mod C's shared memory.  Movers come from rows >= budget, holes are
 // rows < budget, so no move can overwrite another's source and they all run
 // at once.
 //
 // Bound: the latency of the passes for few rows (each a few shared-memory
-// round trips and a cluster barrier); 8 bytes per row plus the moved rows
-// beyond that.
+// round trips and a barrier); 8 bytes per row plus the moved rows beyond that.
 constexpr int EV_THREADS = 512;
-constexpr int EV_SLICE = 32768;    // most rows of one CTA (64 per thread: one flag word)
+constexpr int EV_SLICE = 32768;    // most rows of one CTA (64 steps of a warp: one flag word)
 constexpr int EV_MAX_CLUSTER = 8;
 constexpr int EV_BINS = 2048;
 
@@ -340,9 +339,33 @@ __device__ __forceinline__ unsigned block_prefix(unsigned v, unsigned* sh, unsig
   total = sum;
   return base + x - v;
 }
+// The same over the warps, for a value that is the same in all lanes.
+__device__ __forceinline__ unsigned warp_prefix(unsigned v, unsigned* sh, unsigned& total) {
+  const int w = threadIdx.x >> 5;
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[w] = v;
+  __syncthreads();
+  unsigned base = 0, sum = 0;
+#pragma unroll
+  for (int i = 0; i < EV_THREADS / 32; ++i) {
+    const unsigned y = sh[i];
+    if (i < w) base += y;
+    sum += y;
+  }
+  total = sum;
+  return base;
+}
 __device__ __forceinline__ unsigned dsmem_ldu(uint32_t addr) {
   unsigned v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 dsmem_ld4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ void dsmem_stu(uint32_t addr, unsigned v) {
@@ -350,7 +373,7 @@ __device__ __forceinline__ void dsmem_stu(uint32_t addr, unsigned v) {
 }
 
 __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const EvictArgs a) {
-  extern __shared__ uint32_t sm[];
+  extern __shared__ __align__(16) uint32_t sm[];
   uint32_t* key = sm;                               // [slice_cap]; later the two lists
   uint32_t* hist = sm + a.slice_cap;                // two buffers of EV_BINS
   uint32_t* scan = hist + 2 * EV_BINS;              // [64] block scans
@@ -360,6 +383,10 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const EvictArgs a) {
   const int C = (int)cluster_size(), z = (int)cluster_rank();
   const int pair = blockIdx.x / C, b = pair / a.c.n_kv, g = pair % a.c.n_kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto sync_cluster = [&]() {
+    if (C > 1) cluster_sync_all();
+    else __syncthreads();
+  };
   const int cap = min(a.max_kv, a.c.table_stride << a.c.ps_log2);
   const int L = min(max(__ldg(a.kv_len + b), 0), cap);
   if (g == 0 && z == 0 && tid == 0) a.new_len[b] = min(L, a.budget);
@@ -369,16 +396,35 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const EvictArgs a) {
   const long long fresh = (long long)__ldg(a.next_pos + b) - a.recent;
   for (int i = tid; i < 2 * EV_BINS; i += EV_THREADS) hist[i] = 0u;
   __syncthreads();
-  for (int i = tid; i < n; i += EV_THREADS) {
-    const int r = r0 + i, page = cache_page(a.c, b, r);
-    uint32_t k = 0u;
-    if (page >= 0) {
-      const size_t at = cache_row(a.c, page, g, r);
-      const int p = a.c.pos[at];
-      k = (p < a.sinks || p >= fresh) ? 0xffffffffu : evict_key(a.c.weight[at]);
+  // four rows a thread at a time: their pages, then their positions and weights
+  constexpr int LD = 4;
+  for (int i0 = tid; i0 < n; i0 += EV_THREADS * LD) {
+    int page[LD], pos[LD];
+    float w[LD];
+#pragma unroll
+    for (int k = 0; k < LD; ++k) {
+      const int i = i0 + k * EV_THREADS;
+      page[k] = i < n ? cache_page(a.c, b, r0 + i) : -1;
     }
-    key[i] = k;
-    atomicAdd(hist + (k >> 21), 1u);
+#pragma unroll
+    for (int k = 0; k < LD; ++k) {
+      pos[k] = 0;
+      w[k] = 0.f;
+      if (page[k] >= 0) {
+        const size_t at = cache_row(a.c, page[k], g, r0 + i0 + k * EV_THREADS);
+        pos[k] = a.c.pos[at];
+        w[k] = a.c.weight[at];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < LD; ++k) {
+      const int i = i0 + k * EV_THREADS;
+      if (i >= n) continue;
+      uint32_t kk = 0u;
+      if (page[k] >= 0) kk = (pos[k] < a.sinks || pos[k] >= fresh) ? 0xffffffffu : evict_key(w[k]);
+      key[i] = kk;
+      atomicAdd(hist + (kk >> 21), 1u);
+    }
   }
   // the budget-th largest key: bits 31..21, 20..10, 9..0
   uint32_t prefix = 0u, want = (uint32_t)a.budget;  // want: keys still to take below `prefix`'s range
@@ -392,17 +438,25 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const EvictArgs a) {
       for (int i = tid; i < n; i += EV_THREADS)
         if ((key[i] >> up) == (prefix >> up)) atomicAdd(h + ((key[i] >> shift) & (bins - 1)), 1u);
     }
-    cluster_sync_all();
-    // thread t holds bins 4t..4t+3 counted from the top
-    unsigned cnt[4], sum = 0;
+    sync_cluster();
+    // thread t holds bins 4t..4t+3 counted from the top, one 16-byte load from
+    // every CTA's histogram, all in flight at once
+    unsigned cnt[4] = {0, 0, 0, 0}, sum = 0;
+    if (tid * 4 < bins) {
+      const uint32_t at = (uint32_t)__cvta_generic_to_shared(h + bins - 4 - tid * 4);
+      uint4 v[EV_MAX_CLUSTER];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int bin = bins - 1 - (tid * 4 + e);
-      cnt[e] = 0;
-      if (bin >= 0)
-        for (int q = 0; q < C; ++q)
-          cnt[e] += dsmem_ldu(dsmem_addr((uint32_t)__cvta_generic_to_shared(h + bin), q));
-      sum += cnt[e];
+      for (int p = 0; p < EV_MAX_CLUSTER; ++p)
+        if (p < C) v[p] = dsmem_ld4(dsmem_addr(at, p));
+#pragma unroll
+      for (int p = 0; p < EV_MAX_CLUSTER; ++p)
+        if (p < C) {
+          cnt[0] += v[p].w;
+          cnt[1] += v[p].z;
+          cnt[2] += v[p].y;
+          cnt[3] += v[p].x;
+        }
+      sum = (cnt[0] + cnt[1]) + (cnt[2] + cnt[3]);
     }
     unsigned total;
     unsigned above = block_prefix(sum, scan, total);
@@ -420,39 +474,47 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const EvictArgs a) {
     // the other buffer is empty for the next pass; this one is cleared for the
     // pass after it once every CTA has read it
     if (pass == 0) {
-      cluster_sync_all();
+      sync_cluster();
       for (int i = tid; i < EV_BINS; i += EV_THREADS) h[i] = 0u;
     }
   }
   // `want` rows whose key is the threshold itself stay, lowest rows first.
-  // Thread t owns the run [t q, (t + 1) q) of the slice (q <= 64).
-  const int q = (n + EV_THREADS - 1) / EV_THREADS;
-  const int i0 = min(tid * q, n), i1 = min(i0 + q, n);
+  // Warp w owns the run [w q 32, (w + 1) q 32) of the slice (q <= 64), 32 rows a
+  // step: ballots rank the rows within a step, a running count over the steps,
+  // block prefixes over the warps and the cluster.
+  const int q = (n + EV_THREADS - 1) / EV_THREADS, i0 = warp * q * 32;
+  const unsigned lt = (1u << lane) - 1u;
   unsigned ties = 0;
-  for (int i = i0; i < i1; ++i) ties += key[i] == prefix;
+  for (int k = 0; k < q; ++k) {
+    const int i = i0 + k * 32 + lane;
+    ties += __popc(__ballot_sync(0xffffffffu, i < n && key[i] == prefix));
+  }
   unsigned cta_ties;
-  unsigned tie = block_prefix(ties, scan, cta_ties);
+  unsigned tie = warp_prefix(ties, scan, cta_ties);
   if (tid == 0) xch[0] = cta_ties;
-  cluster_sync_all();
+  sync_cluster();
   for (int p = 0; p < z; ++p) tie += dsmem_ldu(dsmem_addr((uint32_t)__cvta_generic_to_shared(xch), p));
-  unsigned long long keep = 0ull;
+  unsigned long long keep = 0ull;   // bit k: the row of step k stays
   unsigned holes = 0, movers = 0;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key[i];
-    bool in = k > prefix;
-    if (k == prefix) in = tie++ < want;
-    if (in) keep |= 1ull << (i - i0);
-    if (r0 + i < a.budget) holes += !in;
-    else movers += in;
+  for (int k = 0; k < q; ++k) {
+    const int i = i0 + k * 32 + lane;
+    const uint32_t kk = i < n ? key[i] : 0u;
+    const unsigned at = __ballot_sync(0xffffffffu, i < n && kk == prefix);
+    const bool in = i < n && (kk > prefix || (kk == prefix && tie + __popc(at & lt) < want));
+    tie += __popc(at);
+    if (in) keep |= 1ull << k;
+    const bool low = r0 + i < a.budget;
+    holes += __popc(__ballot_sync(0xffffffffu, i < n && low && !in));
+    movers += __popc(__ballot_sync(0xffffffffu, i < n && !low && in));
   }
   unsigned cta_holes, cta_movers;
-  unsigned hole = block_prefix(holes, scan, cta_holes);
-  unsigned mover = block_prefix(movers, scan, cta_movers);
+  unsigned hole = warp_prefix(holes, scan, cta_holes);
+  unsigned mover = warp_prefix(movers, scan + EV_THREADS / 32, cta_movers);
   if (tid == 0) {
     xch[1] = cta_holes;
     xch[2] = cta_movers;
   }
-  cluster_sync_all();   // also: no CTA reads its keys after this point
+  sync_cluster();   // also: no CTA reads its keys after this point
   unsigned moves = 0;
   for (int p = 0; p < C; ++p) {
     const uint32_t at = dsmem_addr((uint32_t)__cvta_generic_to_shared(xch + 1), p);
@@ -464,20 +526,26 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const EvictArgs a) {
     moves += pm;
   }
   // entry e of the lists: CTA e mod C, slot e / C.  At most min(budget,
-  // L - budget) <= L / 2 entries, so two lists fit the key array.
+  // L - budget) <= L / 2 entries, so two lists fit the key array.  The entries
+  // are row indices of the whole cache (31 bits; all ones: the row does not
+  // exist), looked up here, where every thread has its own.
   const uint32_t lists = (uint32_t)__cvta_generic_to_shared(key);
   const uint32_t half = (uint32_t)(a.slice_cap / 2) * 4u;
-  // the entries are row indices of the whole cache (31 bits; all ones: the row
-  // does not exist), looked up here, where every thread has its own
-  for (int i = i0; i < i1; ++i) {
-    const bool in = (keep >> (i - i0)) & 1ull, low = r0 + i < a.budget;
-    if (in == low) continue;
-    const int page = cache_page(a.c, b, r0 + i);
-    const unsigned at = page < 0 ? 0xffffffffu : (unsigned)cache_row(a.c, page, g, r0 + i);
-    const unsigned e = low ? hole++ : mover++;
-    dsmem_stu(dsmem_addr(low ? lists : lists + half, e % C) + (e / C) * 4u, at);
+  for (int k = 0; k < q; ++k) {
+    const int i = i0 + k * 32 + lane;
+    const bool in = (keep >> k) & 1ull, low = r0 + i < a.budget;
+    const bool is_hole = i < n && low && !in, is_mover = i < n && !low && in;
+    const unsigned hm = __ballot_sync(0xffffffffu, is_hole), mm = __ballot_sync(0xffffffffu, is_mover);
+    if (is_hole || is_mover) {
+      const int page = cache_page(a.c, b, r0 + i);
+      const unsigned at = page < 0 ? 0xffffffffu : (unsigned)cache_row(a.c, page, g, r0 + i);
+      const unsigned e = is_hole ? hole + __popc(hm & lt) : mover + __popc(mm & lt);
+      dsmem_stu(dsmem_addr(is_hole ? lists : lists + half, e % C) + (e / C) * 4u, at);
+    }
+    hole += __popc(hm);
+    mover += __popc(mm);
   }
-  cluster_sync_all();
+  sync_cluster();
   const int mine = ((int)moves - z + C - 1) / C;
   const uint32_t* to_row = key;
   const uint32_t* from_row = key + a.slice_cap / 2;

@@ -449,9 +449,18 @@ extern "C" fm_status fm_cache_evict(const fm_paged_cache* c, const int32_t* kv_l
   k.sinks = sinks;
   k.recent = recent;
   k.row_bytes = c->head_dim * esize(c);
-  // CTAs per (sequence, head): enough that each has at most 4096 rows
+  // CTAs per (sequence, head): a second wave of them never pays for the
+  // barriers (64 pairs of 16,384 rows: 4 CTAs each 66 us, 8 94 us, 2 82 us),
+  // nor do slices under 2,048 rows (64 pairs of 4,096: 2 CTAs 46 us, 1 60, 4
+  // 60); below that, more CTAs share the rows (8 pairs of 16,384: 8 CTAs 38 us,
+  // 4 44, 2 62)
+  int sms = 0;
+  FM_TRY(device_sms(&sms));
   int C = 1;
-  while (C < fm::EV_MAX_CLUSTER && (max_kv + C - 1) / C > 4096) C *= 2;
+  while (C < fm::EV_MAX_CLUSTER &&
+         ((max_kv + C - 1) / C > fm::EV_SLICE ||
+          ((max_kv + C - 1) / C > 2048 && (int64_t)B * c->n_kv_heads * C <= sms)))
+    C *= 2;
   k.slice_cap = ((max_kv + C - 1) / C + 127) & ~63;
   static_assert(FM_MAX_EVICT_ROWS <= fm::EV_SLICE * fm::EV_MAX_CLUSTER, "slice");
   FM_CUDA(fm::set_smem_once(fm::k_cache_evict, fm::evict_smem(fm::EV_SLICE + 128)));
