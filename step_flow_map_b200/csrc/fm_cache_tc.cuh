@@ -385,17 +385,21 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
+        uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll 1
         for (int h = 1; h >= 0; --h) {
-          scores(h);
+          if (h == 0) scores(0);                         // (the second half is still there)
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(s[c]), a.scale_log2, -ref));
-            const float p1 = ex2(fmaf(__uint_as_float(s[c + 1]), a.scale_log2, -ref));
-            ls[c & 2] += p0;
-            ls[(c & 2) + 1] += p1;
+            const uint64_t t =
+                fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, ref2);
+            float p0, p1;
+            unpack2(t, p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            ls[(c >> 1) & 1] = add2(ls[(c >> 1) & 1], pack2(p0, p1));
             pk[c >> 1] = pack_bf16x2(p0, p1);
           }
           tmem_st32(tS + C::P_COL + h * 32, pk);         // over the second half of S
@@ -403,7 +407,9 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
           tc_fence_before();
           mbar_arrive(smem_u32(h ? &p_half[p] : &p_full[p]));
         }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        float l0, l1;
+        unpack2(add2(ls[0], ls[1]), l0, l1);
+        l += l0 + l1;
       }
       if (!PAIR && p >= seg.n) mbar_arrive(smem_u32(&q_empty[0]));   // it had no block
       // ---- the segment's result, one row a thread
