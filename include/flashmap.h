@@ -300,7 +300,9 @@ fm_status fm_verify_greedy_noalloc(const float *target_logits, const int32_t *dr
  *                it and no query sees it.
  * page_size is 16, 32, 64 or 128; head_dim 64 or 128 (bf16), 32, 64 or 128
  * (fp32); every array 16-byte aligned.  Pages may be shared by sequences that
- * only read them.  Sequences of a call are rows 0 .. B-1 of the table,
+ * only read them: append, eviction and attention that accumulates weights write
+ * the pages of their sequences, which then no other sequence of the call holds
+ * (nor the same one twice).  Sequences of a call are rows 0 .. B-1 of the table,
  * B <= FM_MAX_CALL_SEQS. */
 typedef struct {
   int dtype, n_pages, page_size, n_kv_heads, head_dim, table_stride;
@@ -361,14 +363,14 @@ fm_status fm_cache_append(const fm_paged_cache *cache, const fm_append_args *a, 
  *   lse          device [T, n_heads] fp32 log-sum-exp of the scores, or NULL
  * With cache->pos q_pos must be given; without it a new row's position is its
  * cache row, whatever q_pos says.  A query that sees nothing gets zeros and
- * lse -inf.  Rows at or past kv_len and rows that no query of the call
- * sees may hold anything, NaN included; a non-finite value in a row that some
- * query sees can reach the sequence's other queries.  Running maxima, sums
+ * lse -inf.  Rows at or past kv_len may hold anything, NaN included, and so may,
+ * without cache->pos, rows that no query of the call sees; a non-finite value
+ * in any other row can reach all queries of the sequence.  Running maxima, sums
  * and outputs are fp32; bf16 probabilities enter the value product rounded
  * to bf16.  Results do not depend on scheduling.
  * ws: device, 256-byte aligned, at least what fm_cache_attention_workspace
  * says for the same sizes on the current device; its contents need no set-up
- * and mean nothing afterwards.  Calls that may overlap on the device (two
+ * and mean nothing afterwards.  out must not overlap q.  Calls that may overlap on the device (two
  * streams, two graphs) need a workspace each. */
 typedef struct {
   int T, B, n_heads, max_rows, max_kv;

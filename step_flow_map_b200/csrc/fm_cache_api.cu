@@ -379,6 +379,7 @@ extern "C" fm_status fm_cache_attention(const fm_paged_cache* c, const fm_attent
   if (a->T == 0) return FM_OK;
   FM_TRY(check_stride(c, "q", a->q, a->q_stride, a->n_heads, a->T));
   FM_TRY(check_stride(c, "out", a->out, a->out_stride, a->n_heads, a->T));
+  if (a->out == a->q) return set_err(FM_ERR_ARG, "out must not be q");
   if (!ws || ((uintptr_t)ws & 255)) return set_err(FM_ERR_ARG, "workspace must be 256-byte aligned");
   AttnPlan p;
   FM_TRY(plan_attention(c, a, &p));
@@ -395,6 +396,7 @@ extern "C" fm_status fm_cache_attention(const fm_paged_cache* c, const fm_attent
   k.rt = p.rt;
   k.tile_rows = p.tile_rows;
   k.ov = p.ov;
+  k.max_tiles = (int)p.tiles;
   k.q = a->q;
   k.qs = a->q_stride;
   k.os = a->out_stride;

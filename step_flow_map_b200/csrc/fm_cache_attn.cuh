@@ -24,6 +24,7 @@ struct CacheAttnArgs {
   int T, B, n_heads, G, max_rows, max_kv;
   int rt, tile_rows;               // packed rows of a (half) tile that are used; of a tile
   int ov;                          // units a tile's start and end cost beyond its blocks
+  int max_tiles;                   // entries of the plan
   const void* q;
   int64_t qs, os;
   const int *cu, *kv_len, *q_pos;
@@ -32,7 +33,7 @@ struct CacheAttnArgs {
   void* out;
   float* lse;                      // or null
   // workspace
-  int* plan_n;                     // [0]: number of tiles, [1]: status of the call
+  int* plan_n;                     // number of tiles
   int* plan_first;                 // [tiles + 1]: first unit of each tile, heads apart
   int4* plan_tile;                 // [tiles][2]: (b, first packed row, first new row, packed rows
                                    //   of the sequence), (s_end, lo, hi, position of new row 0)
@@ -92,6 +93,8 @@ __device__ __forceinline__ size_t score_at(const CacheAttnArgs& a, int b, int g,
 
 // ------------------------------------------------------------------ plan
 // One CTA lists the tiles of every sequence and prefix-sums their blocks.
+// Sequences that overlap, against the rules, can ask for more tiles than the
+// plan holds: the sums stop there.
 constexpr int CP_THREADS = 1024;
 template <int KB>
 __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a) {
@@ -104,24 +107,25 @@ __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a
   if (tid < 256) {
     int n = 0;
     if (tid < a.B) n = min(new_rows(a.cu, a.kv_len, tid, a.T).n, a.max_rows);
-    s_tiles[tid + 1] = (n * a.G + QT - 1) / QT;
+    s_tiles[tid + 1] = min((n * a.G + QT - 1) / QT, a.max_tiles);
   }
   if (tid == 0) s_tiles[0] = 0;
   __syncthreads();
   if (warp == 0) {                 // prefix sum, eight sequences a lane
     int v[8], sum = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += v[k] = s_tiles[lane * 8 + k + 1];
+    for (int k = 0; k < 8; ++k) sum = min(sum + (v[k] = s_tiles[lane * 8 + k + 1]), a.max_tiles);
     int at = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, at, o);
-      if (lane >= o) at += y;
+      if (lane >= o) at = min(at + y, a.max_tiles);
     }
-    at -= sum;
+    at = __shfl_up_sync(0xffffffffu, at, 1);
+    if (lane == 0) at = 0;
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s_tiles[lane * 8 + k + 1] = at += v[k];
+    for (int k = 0; k < 8; ++k) s_tiles[lane * 8 + k + 1] = at = min(at + v[k], a.max_tiles);
   }
   __syncthreads();
   const int E = s_tiles[256];
@@ -161,7 +165,6 @@ __global__ void __launch_bounds__(CP_THREADS) k_cache_plan(const CacheAttnArgs a
   if (tid == 0) {
     a.plan_first[E] = base;
     a.plan_n[0] = E;
-    a.plan_n[1] = 0;
   }
 }
 
@@ -388,14 +391,14 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
       if (r >= rows) continue;
       if (whole) {
         const int x = x0 + r, t = row0 + x / a.G, h = g * a.G + x % a.G;
-        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+        const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
         T* dst = (T*)a.out + t * a.os + h * DH;
 #pragma unroll
         for (int c = 0; c < C::CPT; ++c)
           dst[(c / VW) * VW * C::TC + tc * VW + c % VW] = from_f<T>(o[i][c] * inv);
         if (a.lse && tc == 0)
           a.lse[(size_t)t * a.n_heads + h] =
-              l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
+              l[i] != 0.f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
       } else {
         const size_t p = ((size_t)blockIdx.x * 2 + slot) * QT + r;
 #pragma unroll
@@ -417,7 +420,7 @@ constexpr int CJ_THREADS = 128;
 
 __device__ __forceinline__ void join_store_lse(const CacheAttnArgs& a, int t, int h, float m, float l) {
   if (a.lse)
-    a.lse[(size_t)t * a.n_heads + h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    a.lse[(size_t)t * a.n_heads + h] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // Partials [row][column] (tiles of at most 64 rows): a CTA per packed row, its
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(CJ_THREADS) k_cache_join_rows(const CacheAttnA
   const int col = threadIdx.x;
   l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
   const int t = jb.x + x / a.G, h = jb.y * a.G + x % a.G;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
   if (col < DH)
     ((T*)a.out)[t * a.os + h * DH + col] =
         from_f<T>(((s_o[0][col] + s_o[1][col]) + (s_o[2][col] + s_o[3][col])) * inv);
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(CJ_THREADS) k_cache_join_cols(const CacheAttnA
 #pragma unroll
     for (int k = 0; k < COLS; ++k) o[k] = fmaf(p[(size_t)k * QT], f, o[k]);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
   const int t = jb.x + x / a.G, h = jb.y * a.G + x % a.G;
   bf16* dst = (bf16*)a.out + t * a.os + h * DH + c0;
 #pragma unroll

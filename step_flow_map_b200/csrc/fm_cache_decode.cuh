@@ -116,7 +116,6 @@ __global__ void __launch_bounds__(CD_THREADS, 2) k_cache_decode(const CacheAttnA
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0 && tid == 0) a.plan_n[1] = 0;
   decode_scan<CD_KB>(a, s, s_scan);
   const WorkRun w(s.first[256] * a.c.n_kv, gridDim.x);
   if ((int)blockIdx.x >= w.g || w.N == 0) {
@@ -344,13 +343,13 @@ __global__ void __launch_bounds__(CD_THREADS, 2) k_cache_decode(const CacheAttnA
             acc[k] = fmaf(merge[(i * 4 + warp) * C::MLD + lane * (DH / 32) + k], f[i], acc[k]);
         if (whole) {
           const int t = row0 + x / a.G, h = g * a.G + x % a.G;
-          const float inv = ll > 0.f ? 1.f / ll : 0.f;
+          const float inv = ll != 0.f ? 1.f / ll : 0.f;
           uint32_t* dst = (uint32_t*)((bf16*)a.out + t * a.os + h * DH) + lane * (DH / 64);
 #pragma unroll
           for (int k = 0; k < DH / 64; ++k) dst[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
           if (a.lse && lane == 0)
             a.lse[(size_t)t * a.n_heads + h] =
-                ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+                ll != 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
         } else {
           const size_t p = ((size_t)blockIdx.x * 2 + slot) * CD_QT + x;
 #pragma unroll

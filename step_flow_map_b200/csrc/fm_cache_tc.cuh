@@ -20,7 +20,7 @@
 // by more than 2^8 since the reference in use: p stays below 2^8, which costs
 // no precision in bf16 or fp32.  Every wait is bounded; a thread whose wait
 // gave up goes on through the same barriers (later waits end at once) and the
-// workspace's status word is set.
+// outputs that it may have spoilt are NaN.
 #pragma once
 #include "fm_cache_attn.cuh"
 #include "fm_ptx.cuh"
@@ -29,7 +29,6 @@ namespace fm {
 
 constexpr int CT_THREADS = 384;
 constexpr int CT_KB = 128;
-constexpr int CT_ERR_TIMEOUT = 1;
 
 template <int DH>
 struct CtCfg {
@@ -441,12 +440,13 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         if (!whole) a.part_ml[prt * QT + pr] = make_float2(mm, ll);
         else if (a.lse)
           a.lse[(size_t)t * a.n_heads + hq] =
-              ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+              ll != 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
       };
       if (PAIR || p == 0 || seg.n > 1) (void)mbar_wait(smem_u32(&o_full[p]), oc++ & 1, abort);
       tc_fence_after();
+      if (*abort) l = NAN;                              // a wait gave up: no result, and none to trust
       if constexpr (PAIR) {
-        const float f = l > 0.f ? 1.f / l : 0.f;
+        const float f = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
         for (int c = 0; c < DH; c += 32) {
           uint32_t o[32];
@@ -478,7 +478,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             const float mm = fmaxf(m, o1.x), rf = mm == -INFINITY ? 0.f : mm;
             const float f0 = ex2(m - rf), f1 = seg.n > 1 ? ex2(o1.x - rf) : 0.f;
             const float ll = l * f0 + (seg.n > 1 ? o1.y * f1 : 0.f);
-            const float f = ll > 0.f ? 1.f / ll : 0.f;
+            const float f = ll != 0.f ? 1.f / ll : 0.f;
 #pragma unroll 1
             for (int c = 0; c < DH / 2; c += 32) {
               uint32_t o[32];
@@ -506,7 +506,6 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
   tc_fence_before();
   __syncthreads();
   if (*abort) {
-    if (tid == 0) atomicExch(a.plan_n + 1, CT_ERR_TIMEOUT);
     // let copies and MMAs already issued land before the memory goes away
     const unsigned long long t0 = gtimer();
     while (gtimer() - t0 < 50000ull) {

@@ -30,7 +30,7 @@ def append_args(**kw):
 
 def attn_args(**kw):
     d = dict(T=3, B=2, n_heads=4, max_rows=2, max_kv=64, q=P, q_stride=256, cu_rows=P, kv_len=P,
-             q_pos=P, scale=0.125, out=P, out_stride=256)
+             q_pos=P, scale=0.125, out=P + 4096, out_stride=256)
     return fmb.fm_attention_args(**{**d, **kw})
 
 
@@ -88,6 +88,26 @@ def test_accumulate_without_weights_and_bad_workspace_are_refused():
     refused(fmb.FM_ERR_ARG, fmb.fm_cache_attention, cache(weight=None), attn_args(accumulate=1), P, 1 << 40)
     refused(fmb.FM_ERR_ARG, fmb.fm_cache_attention, cache(), attn_args(), None, 1 << 40)
     refused(fmb.FM_ERR_ARG, fmb.fm_cache_attention, cache(), attn_args(), P + 16, 1 << 40)
+
+
+def test_attention_in_place_is_refused():
+    refused(fmb.FM_ERR_ARG, fmb.fm_cache_attention, cache(), attn_args(out=P, q=P), P, 1 << 40)
+
+
+def test_a_cache_off_the_gpu_is_refused_before_any_launch():
+    k = torch.zeros(6, 2, 16, 64, dtype=torch.bfloat16)
+    pos, weight = torch.zeros(6, 2, 16, dtype=torch.int32), torch.zeros(6, 2, 16)
+    c = PagedCache(k, k.clone(), torch.zeros(2, 3, dtype=torch.int32), pos, weight)
+    cu, kv = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    q, kr = torch.zeros(4, 4, 64, dtype=torch.bfloat16), torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    qp = torch.zeros(4, dtype=torch.int32)
+    for stream in (None, 0):
+        with pytest.raises(ValueError, match="GPU"):
+            c.append(q, kr, kr, cu, kv, q_pos=qp, stream=stream)
+        with pytest.raises(ValueError, match="GPU"):
+            c.attend(q, cu, kv, max_rows=4, max_kv=16, q_pos=qp, stream=stream)
+        with pytest.raises(ValueError, match="GPU"):
+            c.evict(kv, kv, 8, max_kv=16, stream=stream)
 
 
 @pytest.mark.parametrize("a,status", [

@@ -461,3 +461,47 @@ def test_rounds_of_append_attend_evict(dtype):
         for b in range(B):
             for t, buf in zip(state[b], (w.k, w.v, w.pos, w.weight)):
                 assert np.array_equal(w.get(buf, b, lens[b]), t[:lens[b]])
+
+
+# ------------------------------------------------------------------ calls that nothing above makes
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 17, 150])
+def test_a_nan_query_spoils_its_own_row_alone(dtype, rows):
+    """Its output and its lse are NaN, as the formula's; every other row is as without it."""
+    w = World([700, 260], 2, 64, 16, dtype, seed=rows)
+    q = torch.tensor(w.rng.normal(size=(2 * rows, 8, 64))).to(DT[dtype]).cuda()
+    args = dict(max_rows=rows, max_kv=700, lse=True)
+    want, wl = w.cache.attend(q, cu_of([rows, rows]), w.kv, **args)
+    bad = q.clone()
+    bad[rows - 1, 3, 5] = float("nan")
+    got, gl = w.cache.attend(bad, cu_of([rows, rows]), w.kv, **args)
+    assert got[rows - 1, 3].isnan().all() and gl[rows - 1, 3].isnan()
+    got[rows - 1, 3], gl[rows - 1, 3] = want[rows - 1, 3], wl[rows - 1, 3]
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_tiles_than_a_call_can_have_are_cut_off(dtype):
+    """cu_rows that goes back, so that every sequence claims all rows: no error to return (it
+    lies on the device), but nothing out of range is touched and the next call is right."""
+    B, rows = 40, 300
+    w = World([rows] * B, 1, 64, 16, dtype, seed=3)
+    q = torch.tensor(w.rng.normal(size=(rows, 8, 64))).to(DT[dtype]).cuda()
+    cu = torch.tensor([0, rows] * (B // 2) + [0], dtype=torch.int32).cuda()
+    w.cache.attend(q, cu, w.kv, max_rows=rows, max_kv=rows)
+    torch.cuda.synchronize()
+    w = World([rows], 1, 64, 16, dtype, seed=4)
+    check_attention(w, [rows], 8)
+
+
+def test_a_stream_of_another_kind_of_handle():
+    """A raw stream number serves as a stream object does."""
+    w = World([90], 2, 64, 16, "bf16")
+    q = torch.randn(3, 4, 64, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    a = w.cache.attend(q, cu_of([3]), w.kv, max_rows=3, max_kv=90)
+    torch.cuda.synchronize()
+    b = w.cache.attend(q, cu_of([3]), w.kv, max_rows=3, max_kv=90, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(a, b)
