@@ -188,12 +188,16 @@ class PagedCache:
     def _on(self, stream):
         """A context under which tensors are allocated on the cache's device and on
         `stream` (None: the device's current stream), and that stream."""
+        if self.device.type != "cuda":
+            raise ValueError(f"the cache is on {self.device}; its operators run on a GPU")
         if stream is None:   # (the public accessors cost 5 us, as much as a small call's kernels)
             dev = self.device.index
             st = torch._C._cuda_getCurrentRawStream(dev)
             return (_HERE if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)), st
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
+        elif stream.device != self.device:
+            raise ValueError(f"stream of {stream.device}, cache on {self.device}")
         return torch.cuda.stream(stream), stream.cuda_stream
 
     def append(self, q, k, v, cu_rows, kv_len, q_pos=None, *, q_gain=None, k_gain=None, eps=1e-6,
@@ -216,7 +220,7 @@ class PagedCache:
         ctx, st = self._on(stream)
         with ctx:
             if out is None:
-                out = torch.empty((T, n_heads, dh), dtype=q.dtype, device=self.device)
+                out = q.new_empty(T, n_heads, dh)
             os = self._rows("out", out, T, n_heads)
             # positional, in the structure's order
             fm_cache_append(self._c, fm_append_args(
@@ -239,9 +243,9 @@ class PagedCache:
         ctx, st = self._on(stream)
         with ctx:
             if out is None:
-                out = torch.empty((T, n_heads, dh), dtype=q.dtype, device=self.device)
+                out = q.new_empty(T, n_heads, dh)
             os = self._rows("out", out, T, n_heads)
-            got = torch.empty((T, n_heads), dtype=torch.float32, device=self.device) if lse else None
+            got = q.new_empty((T, n_heads), dtype=torch.float32) if lse else None
             a = fm_attention_args(
                 T, B, n_heads, max_rows, max_kv, q.data_ptr(), qs, cu_rows.data_ptr(),
                 kv_len.data_ptr(), None if q_pos is None else q_pos.data_ptr(),
@@ -254,7 +258,7 @@ class PagedCache:
                 if len(self._ws_bytes) > 256:
                     self._ws_bytes.clear()
                 ws_bytes = self._ws_bytes[key] = fm_cache_attention_workspace(self._c, a)
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device)
+            ws = self._table.new_empty(ws_bytes // 4)   # int32; (new_empty parses its arguments fastest)
             fm_cache_attention(self._c, a, ws, ws_bytes, st)
         return (out, got) if lse else out
 
@@ -269,7 +273,7 @@ class PagedCache:
         ctx, st = self._on(stream)
         with ctx:
             if new_len is None:
-                new_len = torch.empty((B,), dtype=torch.int32, device=self.device)
+                new_len = kv_len.new_empty(B)
             else:
                 self._check("new_len", new_len, torch.int32, (B,))
             fm_cache_evict(self._c, kv_len.data_ptr(), next_pos.data_ptr(), B, max_kv, budget, sinks,
