@@ -179,9 +179,9 @@ namespace {
 
 // What a call runs and where its workspace parts lie.
 struct AttnPlan {
-  // bf16: k_cache_decode up to 16 packed rows of a key/value head (its MMA's
-  // M), else k_cache_attn_tc, in pairs of 128-row tiles past 128 rows; fp32:
-  // k_cache_attn_simt with 16- or 64-row tiles
+  // k_cache_decode up to 16 packed rows of a key/value head (its MMA's M); past
+  // that bf16: k_cache_attn_tc, in pairs of 128-row tiles past 128 rows; fp32:
+  // k_cache_attn_simt
   enum { DECODE, TC_ONE, TC_PAIR, SIMT } kind = SIMT;
   int qt = 0, rt = 0, tile_rows = 0, ov = 0, grid = 0;   // rows of a partial; see CacheAttnArgs
   int64_t tiles = 0;
@@ -208,10 +208,11 @@ fm_status plan_attention(const fm_paged_cache* c, const fm_attention_args* a, At
   FM_TRY(device_sms(&sms));
   const int64_t G = a->n_heads / c->n_kv_heads;
   const int64_t rows = a->max_rows * G;
-  p->qt = p->rt = p->tile_rows = rows <= 16 ? 16 : 64;
-  p->grid = 2 * sms;
+  p->kind = rows <= 16 ? AttnPlan::DECODE : AttnPlan::SIMT;
+  p->qt = p->rt = p->tile_rows = rows <= 16 ? fm::CD_QT : fm::CS_QT;
+  // resident CTAs: shared memory holds one of the fp32 kernels of width 128 per SM
+  p->grid = (c->dtype == FM_F32 && c->head_dim == 128 ? 1 : 2) * sms;
   if (c->dtype == FM_BF16) {
-    p->kind = AttnPlan::DECODE;
     if (rows > 16) {
       // whole queries per 128-row tile, so that one TMA box brings them
       p->rt = (int)(128 / G * G);
@@ -251,32 +252,34 @@ fm_status plan_attention(const fm_paged_cache* c, const fm_attention_args* a, At
   return FM_OK;
 }
 
-template <typename T, int DH, int QT>
+template <int DH>
 fm_status launch_simt(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_t st) {
-  using C = fm::CsCfg<DH, QT>;
-  FM_CUDA(fm::set_smem_once(fm::k_cache_attn_simt<T, DH, QT>, C::SMEM));
+  using C = fm::CsCfg<DH>;
+  FM_CUDA(fm::set_smem_once(fm::k_cache_attn_simt<DH>, C::SMEM));
   FM_LAUNCH_OK("cache attention plan",
                fm::launch_pdl(fm::k_cache_plan<fm::CS_KB>, dim3(1), dim3(fm::CP_THREADS), 0, st, k));
-  FM_LAUNCH_OK("cache attention", fm::launch_pdl(fm::k_cache_attn_simt<T, DH, QT>, dim3(p.grid),
+  FM_LAUNCH_OK("cache attention", fm::launch_pdl(fm::k_cache_attn_simt<DH>, dim3(p.grid),
                                                  dim3(fm::CS_THREADS), C::SMEM, st, k));
+  // a warp per row
+  const unsigned rows = (unsigned)std::min<int64_t>(fm::CS_QT, (int64_t)k.max_rows * k.G);
   FM_LAUNCH_OK("cache attention join",
-               fm::launch_pdl(fm::k_cache_join_rows<T, DH, QT>, dim3(p.grid - 1, (unsigned)std::min<int64_t>(QT, (int64_t)k.max_rows * k.G)),
+               fm::launch_pdl(fm::k_cache_join_rows<float, DH, fm::CS_QT>, dim3(p.grid - 1, (rows + 3) / 4),
                               dim3(fm::CJ_THREADS), 0, st, k));
   return FM_OK;
 }
 
-template <int DH>
+template <typename T, int DH>
 fm_status launch_decode(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_t st) {
-  using C = fm::CdCfg<DH>;
-  FM_CUDA(fm::set_smem_once(fm::k_cache_decode<DH>, C::SMEM));
+  using C = fm::CdCfg<T, DH>;
+  FM_CUDA(fm::set_smem_once(fm::k_cache_decode<T, DH>, C::SMEM));
   // no more CTAs than units
   const int64_t units = (int64_t)k.B * k.c.n_kv * ((k.max_kv + fm::CD_KB - 1) / fm::CD_KB + 1);
   const int grid = (int)std::min<int64_t>(p.grid, units);
-  FM_LAUNCH_OK("cache attention", fm::launch_pdl(fm::k_cache_decode<DH>, dim3(grid),
+  FM_LAUNCH_OK("cache attention", fm::launch_pdl(fm::k_cache_decode<T, DH>, dim3(grid),
                                                  dim3(fm::CD_THREADS), C::SMEM, st, k));
   if (grid > 1)
     FM_LAUNCH_OK("cache attention join",
-                 fm::launch_pdl(fm::k_cache_join_rows<bf16, DH, fm::CD_QT>,
+                 fm::launch_pdl(fm::k_cache_join_rows<T, DH, fm::CD_QT>,
                                 dim3(grid - 1, (unsigned)(k.max_rows * k.G)), dim3(fm::CJ_THREADS), 0,
                                 st, k));
   return FM_OK;
@@ -331,12 +334,11 @@ fm_status launch_tc(const fm::CacheAttnArgs& k, const AttnPlan& p, cudaStream_t 
 template <typename T, int DH>
 fm_status run_attention(const fm::CacheAttnArgs& k, const AttnPlan& p, int accumulate,
                         cudaStream_t st) {
-  if constexpr (std::is_same<T, bf16>::value) {
-    if (p.kind == AttnPlan::DECODE) FM_TRY(launch_decode<DH>(k, p, st));
-    else if (p.kind == AttnPlan::TC_ONE) FM_TRY((launch_tc<DH, false>(k, p, st)));
+  if (p.kind == AttnPlan::DECODE) FM_TRY((launch_decode<T, DH>(k, p, st)));
+  else if constexpr (std::is_same<T, bf16>::value) {
+    if (p.kind == AttnPlan::TC_ONE) FM_TRY((launch_tc<DH, false>(k, p, st)));
     else FM_TRY((launch_tc<DH, true>(k, p, st)));
-  } else if (p.qt == 16) FM_TRY((launch_simt<T, DH, 16>(k, p, st)));
-  else FM_TRY((launch_simt<T, DH, 64>(k, p, st)));
+  } else FM_TRY((launch_simt<DH>(k, p, st)));
   if (!accumulate) return FM_OK;
   // at least two waves of CTAs where the rows allow it
   auto grid = [&](int per) {

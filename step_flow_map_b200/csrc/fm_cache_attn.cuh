@@ -16,6 +16,7 @@
 // kernel joins the partials of split tiles in CTA order.
 #pragma once
 #include "fm_cache.cuh"
+#include "fm_ptx.cuh"
 
 namespace fm {
 
@@ -216,32 +217,35 @@ __device__ __forceinline__ void put_join(const CacheAttnArgs& a, const WorkRun& 
 }
 
 // ------------------------------------------------------------------ CUDA-core kernel (fp32)
-// Thread grid TR x TC over a tile of QT packed rows and blocks of 64 cache
-// rows; scores, probabilities and O stay fp32.  Bound: FP32 FMA issue for
-// prompts, HBM for few rows (hence the 16-row tile next to the 64-row one).
-constexpr int CS_THREADS = 128;
+// More than 16 packed rows in fp32: tiles of 64 packed rows against blocks of
+// 64 cache rows, 16 x 16 threads with 4 x 4 scores and 4 x DH / 16 outputs
+// each; scores, probabilities and O stay fp32.  The next block's keys and
+// values come by cp.async while this one is worked on, one CTA barrier a block.
+// Bound: FP32 FMA issue (12 shared-memory wavefronts per 64 FMA instructions of
+// a warp).
+constexpr int CS_THREADS = 256;
 constexpr int CS_KB = 64;
+constexpr int CS_QT = 64;
 
-template <int DH, int QT>
+template <int DH>
 struct CsCfg {
-  static constexpr int TC = QT == 64 ? 8 : 16, TR = CS_THREADS / TC;
-  static constexpr int RPT = QT / TR, KPT = CS_KB / TC, CPT = DH / TC;
+  static constexpr int TC = 16, TR = CS_THREADS / TC;
+  static constexpr int RPT = CS_QT / TR, KPT = CS_KB / TC, CPT = DH / TC;
   static constexpr int LD = DH + 4, PLD = CS_KB + 4;
-  static constexpr int SMEM = (QT * LD + CS_KB * LD + CS_KB * DH + QT * PLD + 2 * CS_KB) * 4;
+  static constexpr int STAGE = CS_KB * (LD + DH + 2);  // keys, values, positions, "exists"
+  static constexpr int SMEM = (CS_QT * LD + 2 * STAGE + CS_QT * PLD) * 4;
 };
 
-template <typename T, int DH, int QT>
-__global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnArgs a) {
-  using C = CsCfg<DH, QT>;
-  constexpr int VE = Vec16<T>::N;
+template <int DH>
+__global__ void __launch_bounds__(CS_THREADS, DH == 128 ? 1 : 2) k_cache_attn_simt(const CacheAttnArgs a) {
+  using C = CsCfg<DH>;
   constexpr int VW = C::CPT < 4 ? C::CPT : 4;      // neighbouring O columns of a thread
-  extern __shared__ float smf[];
+  constexpr int CH = DH / 4;                       // 16-byte pieces of a row
+  extern __shared__ __align__(16) float smf[];
   float* sq = smf;                                 // [QT][LD]
-  float* sk = sq + QT * C::LD;                     // [KB][LD]
-  float* sv = sk + CS_KB * C::LD;                  // [KB][DH]
-  float* sp = sv + CS_KB * DH;                     // [QT][PLD]
-  int* s_pos = (int*)(sp + QT * C::PLD);           // [KB]
-  int* s_ok = s_pos + CS_KB;                       // [KB]
+  float* ring = sq + CS_QT * C::LD;                // two stages: keys [KB][LD], values [KB][DH],
+                                                   //   positions [KB], 1 where the row exists [KB]
+  float* sp = ring + 2 * C::STAGE;                 // [QT][PLD]
   const int tid = threadIdx.x, tr = tid / C::TC, tc = tid % C::TC;
   pdl_wait();
   pdl_trigger();
@@ -262,22 +266,38 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
     const int b = pt.x;
     const SeenRows seen = {ps.x, ps.y, ps.z};
     const SeenBlocks<CS_KB> blocks(seen);
-    const int x0 = pt.y, row0 = pt.z, rows = min(QT, pt.w - x0);
+    const int x0 = pt.y, row0 = pt.z, rows = min(CS_QT, pt.w - x0);
     if (u == u0 && tid == 0) put_join(a, w, blockIdx.x, u - j0, nb, row0, g, x0, pt.w);
-    __syncthreads();
-    for (int i = tid; i < QT * (DH / VE); i += CS_THREADS) {
-      const int r = i / (DH / VE), c = (i % (DH / VE)) * VE;
-      float f[VE];
+    auto load = [&](int j) {
+      const int r0 = blocks.row(j);
+      float* st = ring + (j & 1) * C::STAGE;
+      int* info = (int*)(st + CS_KB * (C::LD + DH));
+      const uint32_t k32 = (uint32_t)__cvta_generic_to_shared(st), v32 = k32 + CS_KB * C::LD * 4;
+#pragma unroll
+      for (int i = tid; i < CS_KB * CH; i += CS_THREADS) {
+        const int r = i / CH, c = i % CH, cr = r0 + r;
+        const int page = row_seen(seen, cr) ? cache_page(a.c, b, cr) : -1;
+        const size_t at = cache_row(a.c, max(page, 0), g, cr);
+        cp_async16_if(k32 + (r * C::LD + c * 4) * 4, (const float*)a.c.k + at * DH + c * 4, page >= 0);
+        cp_async16_if(v32 + (r * DH + c * 4) * 4, (const float*)a.c.v + at * DH + c * 4, page >= 0);
+        if (c == 0) {
+          info[r] = a.c.pos && page >= 0 ? a.c.pos[at] : cr;
+          info[CS_KB + r] = page >= 0;
+        }
+      }
+      cp_commit();
+    };
+    __syncthreads();                               // the tile before is done with the buffers
+    load(j0);
+    for (int i = tid; i < CS_QT * CH; i += CS_THREADS) {
+      const int r = i / CH, c = (i % CH) * 4;
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows) {
         const int x = x0 + r;
-        Vec16<T>::unpack(*(const uint4*)((const T*)a.q + (row0 + x / a.G) * a.qs +
-                                         (g * a.G + x % a.G) * DH + c), f);
-      } else {
-#pragma unroll
-        for (int k = 0; k < VE; ++k) f[k] = 0.f;
+        f = *(const float4*)((const float*)a.q + (row0 + x / a.G) * a.qs + (g * a.G + x % a.G) * DH + c);
+        f.x *= a.scale_log2; f.y *= a.scale_log2; f.z *= a.scale_log2; f.w *= a.scale_log2;
       }
-#pragma unroll
-      for (int k = 0; k < VE; ++k) sq[r * C::LD + c + k] = f[k] * a.scale_log2;
+      *(float4*)(sq + r * C::LD + c) = f;
     }
     int pq[C::RPT];
     float m[C::RPT], l[C::RPT], o[C::RPT][C::CPT];
@@ -291,29 +311,20 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
 #pragma unroll
       for (int c = 0; c < C::CPT; ++c) o[i][c] = 0.f;
     }
+    // positions of the tile's first and last query
+    const int pmin = ps.w + x0 / a.G, pmax = ps.w + (x0 + rows - 1) / a.G;
     for (int j = j0; j < j1; ++j) {
       const int r0 = blocks.row(j);
+      cp_wait<0>();
       __syncthreads();
-      for (int i = tid; i < CS_KB * (DH / VE); i += CS_THREADS) {
-        const int r = i / (DH / VE), c = (i % (DH / VE)) * VE, cr = r0 + r;
-        const int page = row_seen(seen, cr) ? cache_page(a.c, b, cr) : -1;
-        float fk[VE], fv[VE];
-#pragma unroll
-        for (int k = 0; k < VE; ++k) fk[k] = fv[k] = 0.f;
-        if (page >= 0) {
-          const size_t at = cache_row(a.c, page, g, cr);
-          Vec16<T>::unpack(*(const uint4*)((const T*)a.c.k + at * DH + c), fk);
-          Vec16<T>::unpack(*(const uint4*)((const T*)a.c.v + at * DH + c), fv);
-          if (c == 0) s_pos[r] = a.c.pos ? a.c.pos[at] : cr;
-        }
-        if (c == 0) s_ok[r] = page >= 0;
-#pragma unroll
-        for (int k = 0; k < VE; ++k) {
-          sk[r * C::LD + c + k] = fk[k];
-          sv[r * DH + c + k] = fv[k];
-        }
-      }
-      __syncthreads();
+      if (j + 1 < j1) load(j + 1);
+      const float* sk = ring + (j & 1) * C::STAGE;
+      const float* sv = sk + CS_KB * C::LD;
+      const int* s_pos = (const int*)(sv + CS_KB * DH);
+      const int* s_ok = s_pos + CS_KB;
+      // every row that exists is seen by every query
+      const bool open = !a.c.pos && r0 >= seen.lo && r0 + CS_KB <= seen.hi && r0 + CS_KB - 1 <= pmin &&
+                        (a.window == 0 || pmax - r0 < a.window);
       float sc[C::RPT][C::KPT];
 #pragma unroll
       for (int i = 0; i < C::RPT; ++i)
@@ -342,9 +353,7 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
 #pragma unroll
         for (int k = 0; k < C::KPT; ++k) {
           const int kr = tc + C::TC * k;
-          if (!(s_ok[kr] && sees(pq[i], s_pos[kr], a.window, a.sinks))) sc[i][k] = -INFINITY;
-          if (QT == 16 && a.scores && tr + C::TR * i < rows && row_seen(seen, r0 + kr))
-            a.scores[score_at(a, b, g, r0 + kr, tr + C::TR * i)] = sc[i][k];
+          if (!s_ok[kr] || !(open || sees(pq[i], s_pos[kr], a.window, a.sinks))) sc[i][k] = -INFINITY;
           mx = fmaxf(mx, sc[i][k]);
         }
 #pragma unroll
@@ -363,21 +372,26 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
         }
       }
       __syncwarp();                                // a row's probabilities come from its own warp
-#pragma unroll 4
-      for (int k = 0; k < CS_KB; ++k) {
-        float pv[C::RPT];
+#pragma unroll 2
+      for (int k = 0; k < CS_KB; k += 4) {
+        float4 pv[C::RPT];
 #pragma unroll
-        for (int i = 0; i < C::RPT; ++i) pv[i] = sp[(tr + C::TR * i) * C::PLD + k];
+        for (int i = 0; i < C::RPT; ++i) pv[i] = *(const float4*)(sp + (tr + C::TR * i) * C::PLD + k);
 #pragma unroll
-        for (int c = 0; c < C::CPT; c += VW) {
-          float vv[VW];
+        for (int y = 0; y < 4; ++y)
 #pragma unroll
-          for (int z = 0; z < VW; ++z) vv[z] = sv[k * DH + c * C::TC + tc * VW + z];
+          for (int c = 0; c < C::CPT; c += VW) {
+            float vv[VW];
+            const float* src = sv + (k + y) * DH + c * C::TC + tc * VW;
+            if constexpr (VW == 4) *(float4*)vv = *(const float4*)src;
+            else *(float2*)vv = *(const float2*)src;
 #pragma unroll
-          for (int i = 0; i < C::RPT; ++i)
+            for (int i = 0; i < C::RPT; ++i) {
+              const float p = y == 0 ? pv[i].x : y == 1 ? pv[i].y : y == 2 ? pv[i].z : pv[i].w;
 #pragma unroll
-            for (int z = 0; z < VW; ++z) o[i][c + z] = fmaf(pv[i], vv[z], o[i][c + z]);
-        }
+              for (int z = 0; z < VW; ++z) o[i][c + z] = fmaf(p, vv[z], o[i][c + z]);
+            }
+          }
       }
       __syncwarp();
     }
@@ -392,15 +406,14 @@ __global__ void __launch_bounds__(CS_THREADS) k_cache_attn_simt(const CacheAttnA
       if (whole) {
         const int x = x0 + r, t = row0 + x / a.G, h = g * a.G + x % a.G;
         const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
-        T* dst = (T*)a.out + t * a.os + h * DH;
+        float* dst = (float*)a.out + t * a.os + h * DH;
 #pragma unroll
-        for (int c = 0; c < C::CPT; ++c)
-          dst[(c / VW) * VW * C::TC + tc * VW + c % VW] = from_f<T>(o[i][c] * inv);
+        for (int c = 0; c < C::CPT; ++c) dst[(c / VW) * VW * C::TC + tc * VW + c % VW] = o[i][c] * inv;
         if (a.lse && tc == 0)
           a.lse[(size_t)t * a.n_heads + h] =
               l[i] != 0.f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
       } else {
-        const size_t p = ((size_t)blockIdx.x * 2 + slot) * QT + r;
+        const size_t p = ((size_t)blockIdx.x * 2 + slot) * CS_QT + r;
 #pragma unroll
         for (int c = 0; c < C::CPT; ++c)
           a.part[p * DH + (c / VW) * VW * C::TC + tc * VW + c % VW] = o[i][c];
@@ -423,18 +436,21 @@ __device__ __forceinline__ void join_store_lse(const CacheAttnArgs& a, int t, in
     a.lse[(size_t)t * a.n_heads + h] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Partials [row][column] (tiles of at most 64 rows): a CTA per packed row, its
-// warps take every fourth run.
+// Partials [row][column] (tiles of at most 64 rows).  Few packed rows: a CTA per
+// row, its warps take every fourth run, so that a long cache's many runs are
+// read at once.  64-row tiles: a warp per row (a CTA per row took 18 us for 28
+// tiles of 51 rows, most of it CTAs that come and go).
 template <typename T, int DH, int QT>
 __global__ void __launch_bounds__(CJ_THREADS) k_cache_join_rows(const CacheAttnArgs a) {
-  constexpr int W = CJ_THREADS / 32;
+  constexpr int W = QT == 64 ? 1 : CJ_THREADS / 32;  // warps of a row
   __shared__ float s_l[W], s_o[W][DH];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
   const int4 ja = a.plan_join[2 * blockIdx.x + 2], jb = a.plan_join[2 * blockIdx.x + 3];
-  const int c0 = ja.x, last = ja.y, r = blockIdx.y, x = jb.z + r;
-  if (c0 < 0 || x >= ja.w) return;
+  const int r = W == 1 ? blockIdx.y * (CJ_THREADS / 32) + (threadIdx.x >> 5) : blockIdx.y;
+  const int c0 = ja.x, last = ja.y, x = jb.z + r;
+  if (c0 < 0 || r >= QT || x >= ja.w) return;
   auto at = [&](int i) { return ((size_t)i * 2 + (i == c0 ? ja.z : 0)) * QT + r; };
   float m = -INFINITY;
   for (int i = c0 + lane; i <= last; i += 32) m = fmaxf(m, a.part_ml[at(i)].x);
@@ -452,18 +468,24 @@ __global__ void __launch_bounds__(CJ_THREADS) k_cache_join_rows(const CacheAttnA
 #pragma unroll
     for (int k = 0; k < DH / 32; ++k) o[k] = fmaf(a.part[p * DH + lane + 32 * k], f, o[k]);
   }
-  if (lane == 0) s_l[warp] = l;
-#pragma unroll
-  for (int k = 0; k < DH / 32; ++k) s_o[warp][lane + 32 * k] = o[k];
-  __syncthreads();
-  const int col = threadIdx.x;
-  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
   const int t = jb.x + x / a.G, h = jb.y * a.G + x % a.G;
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  if (col < DH)
-    ((T*)a.out)[t * a.os + h * DH + col] =
-        from_f<T>(((s_o[0][col] + s_o[1][col]) + (s_o[2][col] + s_o[3][col])) * inv);
-  if (threadIdx.x == 0) join_store_lse(a, t, h, m, l);
+  T* const dst = (T*)a.out + t * a.os + h * DH;
+  if constexpr (W == 1) {
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int k = 0; k < DH / 32; ++k) dst[lane + 32 * k] = from_f<T>(o[k] * inv);
+    if (lane == 0) join_store_lse(a, t, h, m, l);
+  } else {
+    if (lane == 0) s_l[warp] = l;
+#pragma unroll
+    for (int k = 0; k < DH / 32; ++k) s_o[warp][lane + 32 * k] = o[k];
+    __syncthreads();
+    const int col = threadIdx.x;
+    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    if (col < DH) dst[col] = from_f<T>(((s_o[0][col] + s_o[1][col]) + (s_o[2][col] + s_o[3][col])) * inv);
+    if (threadIdx.x == 0) join_store_lse(a, t, h, m, l);
+  }
 }
 
 // Partials [column][row] (the 128-row tiles): a lane per row, a warp per
