@@ -27,8 +27,11 @@ constexpr int CD_QT = 16;
 // Where every sequence's units begin, and what it sees.
 struct DecodeSeqs {
   int first[257];                  // prefix sums of blocks (heads apart)
-  int s_end[256], lo[256], hi[256];
+  int lo[256], hi[256];
   int row0[256], n[256], len[256];
+  __device__ __forceinline__ SeenRows seen(const CacheAttnArgs& a, int b) const {
+    return {a.window > 0 && !a.c.pos ? min(a.sinks, lo[b]) : 0, lo[b], hi[b]};   // as seen_rows
+  }
 };
 template <int KB>
 __device__ __forceinline__ void decode_scan(const CacheAttnArgs& a, DecodeSeqs& s, int* sh) {
@@ -43,7 +46,6 @@ __device__ __forceinline__ void decode_scan(const CacheAttnArgs& a, DecodeSeqs& 
       const int n = min(r.n, a.max_rows);
       const SeenRows v = seen_rows(a, r, 0, max(0, n - 1));
       if (n > 0) nb[k] = SeenBlocks<KB>(v).nb;
-      s.s_end[b] = v.s_end;
       s.lo[b] = v.lo;
       s.hi[b] = v.hi;
       s.row0[b] = r.first;
@@ -107,7 +109,7 @@ struct CdCfg {
   static constexpr int MLD = DH + 4;                   // merge buffer row
   // a warp's merge rows (4), which also hold its 16 x 16 probabilities (fp32)
   static constexpr int SLOT = 4 * MLD > 256 ? 4 * MLD : 256;
-  static constexpr int QLD = DH + 8;                   // fp32 query row, its second half 4 on
+  static constexpr int QLD = DH + 4;                   // fp32 query row, its second half 4 on
   static constexpr int SMEM = 4 * RING + 4 * SLOT * 4 + (sizeof(T) == 4 ? 16 * (QLD + 1) * 4 : 0);
   static constexpr int CTAS = SMEM > 110 * 1024 ? 1 : 2;   // per SM
 };
@@ -409,14 +411,14 @@ __global__ void __launch_bounds__(CD_THREADS, (CdCfg<T, DH>::CTAS)) k_cache_deco
   if (tid == 0)
     put_join(a, w, blockIdx.x, u0 - ld.j, ld.nb, s.row0[ld.b], ld.g, 0, s.n[ld.b] * a.G);
   auto tile_row = [&](const DecodeCursor& c) {
-    const SeenRows v = {s.s_end[c.b], s.lo[c.b], s.hi[c.b]};
+    const SeenRows v = s.seen(a, c.b);
     return SeenBlocks<CD_KB>(v).row(c.j) + 16 * warp;
   };
   int ld_row = tile_row(ld), ld_page = cache_page(a.c, ld.b, ld_row);
   // stage `st` <- the load cursor's unit; then the cursor moves on and its
   // page number starts loading
   auto load = [&](int st, bool more) {
-    const SeenRows v = {s.s_end[ld.b], s.lo[ld.b], s.hi[ld.b]};
+    const SeenRows v = s.seen(a, ld.b);
     const uint32_t dst = ring + st * C::STAGE;
     const size_t at = cache_row(a.c, max(ld_page, 0), ld.g, ld_row);
     const char* gk = (const char*)a.c.k + at * C::ROW;
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(CD_THREADS, (CdCfg<T, DH>::CTAS)) k_cache_deco
     const int b = cu.b, g = cu.g, j0 = cu.j, nb = cu.nb;
     const int todo = min(nb - j0, count - done);
     const int rows = s.n[b] * a.G, row0 = s.row0[b], p0 = s.len[b];
-    const SeenRows seen = {s.s_end[b], s.lo[b], s.hi[b]};
+    const SeenRows seen = s.seen(a, b);
     const DecodeTile tile = {rows, row0, p0, p0 + s.n[b] - 1, g, seen};
     DecodeState<T, DH> state;
     state.begin(a, tile, sq);

@@ -5,9 +5,11 @@
 // TMEM), P = 2^(S - m) rounded to bf16 over the second half of S, O += P V with P
 // read from TMEM.  Keys and values come page by page through TMA into a ring
 // of 128-row tiles (128-byte swizzle): K as the K-major operand, V as it lies,
-// MN-major.  Two softmax warpgroups, one thread per packed row, work on two
-// S/O pairs that fill TMEM (2 x (128 + DH) columns), so one's exponentials run
-// under the other's products:
+// MN-major.  Two S/O pairs fill TMEM (2 x (128 + DH) columns), so one's
+// exponentials run under the other's products; two softmax warpgroups work on
+// each, a thread on 64 keys of one packed row (with one warpgroup per pair, a
+// thread on all 128 keys, the chain of loads, maximum, exponentials and stores
+// was 2,900 of a block's 3,900 clocks):
 //   PAIR  (more than 128 packed rows) the pairs are two tiles of 128 rows that
 //         share every K/V tile;
 //   else  one tile of 128 rows: even blocks go to pair 0, odd ones to pair 1,
@@ -15,7 +17,7 @@
 // Bound: for prompts the exponentials (16 a clock and SM) and the products
 // about equally; for drafted blocks HBM.
 //
-// Roles (384 threads): warp 0 TMA, warp 1 MMA, warps 4-7 and 8-11 softmax.
+// Roles (640 threads): warp 0 TMA, warp 1 MMA, warps 4-19 softmax.
 // O is rescaled by the softmax threads, and only when a row maximum has grown
 // by more than 2^8 since the reference in use: p stays below 2^8, which costs
 // no precision in bf16 or fp32.  Every wait is bounded; a thread whose wait
@@ -27,7 +29,7 @@
 
 namespace fm {
 
-constexpr int CT_THREADS = 384;
+constexpr int CT_THREADS = 640;
 constexpr int CT_KB = 128;
 
 template <int DH>
@@ -37,9 +39,9 @@ struct CtCfg {
   static constexpr int STAGES = DH == 128 ? 5 : 8;
   static constexpr int O_COL = 256;                    // TMEM: S0, S1 (128 each), O0, O1
   static constexpr int P_COL = 64;                     // P over the second half of its S
-  static constexpr int BARS = 2 * STAGES + 12;         // full, empty; per pair s_full, p_half,
-                                                       //   p_full, o_full, q_full, q_empty
-  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + 2 * 128 * 4 + 256;
+  static constexpr int BARS = 2 * STAGES + 10;         // full, empty; per pair s_full, p_full,
+                                                       //   o_full, q_full, q_empty
+  static constexpr int SMEM = 2 * TILE + STAGES * TILE + 4 * 128 * 4 + BARS * 8 + 16;
 };
 
 // A stretch of one tile's units inside a CTA's run: nv of them, of which the
@@ -82,15 +84,15 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 const __grid_constant__ CUtensorMap mapQ, const CacheAttnArgs a) {
   using C = CtCfg<DH>;
   constexpr int QT = PAIR ? 256 : 128;                 // partial rows of a tile
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* sQ = base;                                  // two tiles; the second is the merge
-  uint8_t* sKV = base + 2 * C::TILE;                   //   buffer when there is one Q tile
-  int* s_kpos = (int*)(sKV + C::STAGES * C::TILE);     // [2][128] key positions
-  uint64_t* bars = (uint64_t*)(s_kpos + 256);
-  uint64_t *full = bars, *empty = bars + C::STAGES, *s_full = empty + C::STAGES,
-           *p_half = s_full + 2, *p_full = p_half + 2, *o_full = p_full + 2, *q_full = o_full + 2,
-           *q_empty = q_full + 2;
+  extern __shared__ __align__(1024) uint8_t smem_tc[];
+  uint8_t* sQ = smem_tc;                               // two tiles; the second is the merge
+  uint8_t* sKV = sQ + 2 * C::TILE;                     //   buffer when there is one Q tile
+  // [pair][half][row]: row maxima and sums that the halves exchange; stored key
+  // positions of a pair's block lie over its first half's
+  float* s_mx = (float*)(sKV + C::STAGES * C::TILE);
+  uint64_t* bars = (uint64_t*)(s_mx + 512);
+  uint64_t *full = bars, *empty = bars + C::STAGES, *s_full = empty + C::STAGES, *p_full = s_full + 2,
+           *o_full = p_full + 2, *q_full = o_full + 2, *q_empty = q_full + 2;
   uint32_t* tmem_slot = (uint32_t*)(bars + C::BARS);
   volatile int* abort = (volatile int*)(tmem_slot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -102,11 +104,10 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&p_full[i]), 128);
-      mbar_init(smem_u32(&p_half[i]), 128);
+      mbar_init(smem_u32(&p_full[i]), 256);
       mbar_init(smem_u32(&o_full[i]), 1);
       mbar_init(smem_u32(&q_full[i]), 1);
-      mbar_init(smem_u32(&q_empty[i]), PAIR ? 128 : 256);
+      mbar_init(smem_u32(&q_empty[i]), PAIR ? 256 : 512);
     }
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -212,15 +213,13 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         const int c = cnt + 2 * j + 1, st = c % C::STAGES;
         const uint32_t ph = (p ? pc1++ : pc0++) & 1;
         (void)mbar_wait(smem_u32(&full[st]), (c / C::STAGES) & 1, abort);
-        // the block's second 64 keys are ready first
+        (void)mbar_wait(smem_u32(&p_full[p]), ph, abort);
+        tc_fence_after();
 #pragma unroll
-        for (int h = 1; h >= 0; --h) {
-          (void)mbar_wait(smem_u32(h ? &p_half[p] : &p_full[p]), ph, abort);
-          tc_fence_after();
+        for (int h = 0; h < 2; ++h)
           tc_mma4_ts(tmem + C::O_COL + p * 128, tmem + p * 128 + C::P_COL + h * 32,
                      (uint32_t)dv + ((st * C::TILE + h * 64 * 128) >> 4), (uint32_t)(dv >> 32), idO,
-                     s >= 2 || h == 0);
-        }
+                     s >= 2 || h > 0);
         if (!PAIR || p == 1) tc_commit_elect(smem_u32(&empty[st]));
         if (s + 2 >= steps) tc_commit_elect(smem_u32(&o_full[p]));
       };
@@ -243,11 +242,14 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                seg.all);
     }
   } else if (warp >= 4) {
-    // ---------------- softmax: thread = packed row `r` of pair `p`
-    const int p = (warp - 4) >> 2, r = tid & 127;
+    // ---------------- softmax: thread = 64 keys (`half`) of packed row `r` of pair `p`
+    const int p = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, r = tid & 127;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tS = tl + p * 128, tO = tl + C::O_COL + p * 128;
-    const int bar = 1 + p;
+    const uint32_t tS = tl + p * 128, tO = tl + C::O_COL + p * 128 + half * (DH / 2);
+    const int rows_bar = 1 + p * 4 + (warp & 3), pair_bar = 9 + p;   // two warps, eight warps
+    float* const mine = s_mx + (p * 2 + half) * 128 + r;
+    const float* const others = s_mx + (p * 2 + (half ^ 1)) * 128 + r;
+    int* const s_kpos = (int*)(s_mx + p * 256);
     uint32_t sc = 0, oc = 0;                            // phases of s_full and o_full seen
     int cnt = 0;                                        // ring entries of earlier segments
     const int np = CT_KB >> a.c.ps_log2;
@@ -257,15 +259,15 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
       if (seg.n == 0) break;
       const SeenBlocks<CT_KB> blocks(seg.seen);
       const int all = seg.all;
-      const int xw = seg.x0 + (PAIR ? p * a.rt : 0);    // this warpgroup's first packed row
+      const int xw = seg.x0 + (PAIR ? p * a.rt : 0);    // this pair's first packed row
       const int x = xw + r;
       const bool live = r < a.rt && x < all;
       const int qi = live ? x / a.G : 0, hq = seg.g * a.G + (live ? x - qi * a.G : 0);
       const int pq = a.q_pos ? __ldg(a.q_pos + seg.row0 + qi) : seg.p0 + qi;
-      // positions that every row of this warpgroup sees: [.., pmin], window from pmax
+      // positions that every row of this pair sees: [.., pmin], window from pmax
       const int pmin = seg.p0 + min(xw, all - 1) / a.G;
       const int pmax = seg.p0 + (min(xw + a.rt, all) - 1) / a.G;
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f;                     // l: this thread's keys
       bool first = true;
       // lane's page-table entry of a block, loaded one block before it is looked at
       auto page_of = [&](int j) {
@@ -276,36 +278,38 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
       int page = page_of(PAIR ? 0 : p);
       for (int j = PAIR ? 0 : p; j < seg.n; j += PAIR ? 1 : 2) {
         const int r0 = blocks.row(seg.j0 + j);
-        const int ring = cnt + 2 * j + 1;               // the block's V tile
         const uint32_t pages = __ballot_sync(0xffffffffu, (unsigned)page < (unsigned)a.c.n_pages);
         page = page_of(j + (PAIR ? 1 : 2));
         const bool inside = r0 >= seg.seen.lo && r0 + CT_KB <= seg.seen.hi;
         const bool open = !a.c.pos && inside && pages == all_pages && r0 + CT_KB - 1 <= pmin &&
                           (a.window == 0 || pmax - r0 < a.window);
-        unsigned long long see0 = ~0ull, see1 = ~0ull;  // this row's mask of the 128 keys
+        uint32_t see0 = ~0u, see1 = ~0u;                // this thread's mask of its 64 keys
         if (!open) {
           const int kr = r0 + r;
           if (!inside || a.c.pos) {
-            named_sync(bar, 128);                       // the last block's readers are done
-            if (a.c.pos) {
+            named_sync(pair_bar, 256);                  // the last block's readers are done
+            if (a.c.pos && half == 0) {
               int kp = 0;
               if (row_seen(seg.seen, kr) && ((pages >> (r >> a.c.ps_log2)) & 1u))
                 kp = a.c.pos[cache_row(a.c, cache_page(a.c, seg.b, kr), seg.g, kr)];
-              s_kpos[p * 128 + r] = kp;
+              s_kpos[r] = kp;
             }
             // value rows in pages that exist but that nobody sees may hold
             // anything: zero them, as 0 x NaN would not be 0
             if (!inside) {
+              const int ring = cnt + 2 * j + 1;         // the block's V tile
               (void)mbar_wait(smem_u32(&full[ring % C::STAGES]), (ring / C::STAGES) & 1, abort);
               if (!row_seen(seg.seen, kr)) {
                 uint8_t* v = sKV + (ring % C::STAGES) * C::TILE + r * 128;
 #pragma unroll
-                for (int c = 0; c < DH / 8; ++c)        // neighbouring rows on different banks
+                for (int z = 0; z < DH / 16; ++z) {     // neighbouring rows on different banks
+                  const int c = half * (DH / 16) + z;
                   *(uint4*)(v + (c >> 3) * C::BOX + (((c + r) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                }
               }
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
-            named_sync(bar, 128);
+            named_sync(pair_bar, 256);
           }
           // without stored positions a row sees keys [0, c_sink) and [c_lo, c_hi)
           // of the block (counted from r0; r0 and the ends are cache rows, and
@@ -313,55 +317,47 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
           const int c_hi = min(seg.seen.hi, min(pq, seg.seen.hi) + 1) - r0;
           const int c_lo = a.window > 0 && pq >= a.window ? pq - a.window + 1 - r0 : 0;
           const int c_sink = a.window > 0 ? min(a.sinks - r0, c_hi) : 0;
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            const int c0 = h * 64, c = c0 + lane;
-            const uint32_t k0 = __ballot_sync(
-                0xffffffffu, row_seen(seg.seen, r0 + c) && ((pages >> (c >> a.c.ps_log2)) & 1u));
-            const uint32_t k1 = __ballot_sync(
-                0xffffffffu,
-                row_seen(seg.seen, r0 + c + 32) && ((pages >> ((c + 32) >> a.c.ps_log2)) & 1u));
-            unsigned long long mine = 0ull;
-            if (a.c.pos) {
+          const int c0 = half * 64, c = c0 + lane;
+          const uint32_t k0 = __ballot_sync(
+              0xffffffffu, row_seen(seg.seen, r0 + c) && ((pages >> (c >> a.c.ps_log2)) & 1u));
+          const uint32_t k1 = __ballot_sync(
+              0xffffffffu,
+              row_seen(seg.seen, r0 + c + 32) && ((pages >> ((c + 32) >> a.c.ps_log2)) & 1u));
+          unsigned long long see = 0ull;
+          if (a.c.pos) {
 #pragma unroll 4
-              for (int i = 0; i < 64; ++i)
-                mine |= (unsigned long long)sees(pq, s_kpos[p * 128 + c0 + i], a.window, a.sinks) << i;
-            } else {
-              mine = (below(c_hi - c0) & ~below(c_lo - c0)) | below(c_sink - c0);
-            }
-            mine &= (unsigned long long)k1 << 32 | k0;
-            if (h == 0) see0 = mine;
-            else see1 = mine;
+            for (int i = 0; i < 64; ++i)
+              see |= (unsigned long long)sees(pq, s_kpos[c0 + i], a.window, a.sinks) << i;
+            named_sync(pair_bar, 256);                  // the maxima go where the positions are
+          } else {
+            see = (below(c_hi - c0) & ~below(c_lo - c0)) | below(c_sink - c0);
           }
+          see0 = (uint32_t)see & k0;
+          see1 = (uint32_t)(see >> 32) & k1;
         }
         (void)mbar_wait(smem_u32(&s_full[p]), sc & 1, abort);
         ++sc;
         // the tile's last scores are there: its queries may be replaced
         if (j + (PAIR ? 1 : 2) >= seg.n) mbar_arrive(smem_u32(&q_empty[PAIR ? p : 0]));
         tc_fence_after();
-        // 64 scores in registers at a time, first for the maximum, then again
-        // for the exponentials.  (The loops stay rolled: straight-line code of
-        // the whole block no longer fits the instruction caches, and a tile's
-        // prologue and epilogue then run at the speed of their misses.)
         uint32_t s[64];
-        auto scores = [&](int h) {
-          tmem_ld64(tS + h * 64, s);
-          if (!open) {
-            const unsigned long long see = h ? see1 : see0;
-            const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
+        tmem_ld64(tS + half * 64, s);
+        if (!open) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (!(((c < 32 ? lo : hi) >> (c & 31)) & 1u)) s[c] = 0xff800000u;   // -inf
-          }
-        };
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          scores(h);
-#pragma unroll
-          for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+          for (int c = 0; c < 64; ++c)
+            if (!(((c < 32 ? see0 : see1) >> (c & 31)) & 1u)) s[c] = 0xff800000u;   // -inf
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+        const float my_top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        *mine = my_top;
+        // also: both halves of the scores are in registers, P may overwrite them
+        tc_fence_before();
+        named_sync(rows_bar, 64);
+        tc_fence_after();
+        const float top = fmaxf(my_top, *others) * a.scale_log2;
+        // (both halves of a row come to the same m and f)
         const bool grow = !first && __any_sync(0xffffffffu, top > m + 8.f);
         float f = 1.f;
         if (first) {
@@ -373,9 +369,27 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
           l *= f;
         }
         first = false;
+        const float ref = m == -INFINITY ? 0.f : m;
+        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
+        uint64_t ls[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const uint64_t t =
+              fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, ref2);
+          float p0, p1;
+          unpack2(t, p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          ls[(c >> 1) & 1] = add2(ls[(c >> 1) & 1], pack2(p0, p1));
+          s[c >> 1] = pack_bf16x2(p0, p1);
+        }
+        tmem_st32(tS + C::P_COL + half * 32, s);         // over the second half of S
+        float l0, l1;
+        unpack2(add2(ls[0], ls[1]), l0, l1);
+        l += l0 + l1;
         if (grow) {
 #pragma unroll 1
-          for (int c = 0; c < DH; c += 32) {
+          for (int c = 0; c < DH / 2; c += 32) {
             uint32_t o[32];
             tmem_ld32(tO + c, o);
 #pragma unroll
@@ -383,41 +397,19 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             tmem_st32(tO + c, o);
           }
         }
-        const float ref = m == -INFINITY ? 0.f : m;
-        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
-        uint64_t ls[2] = {0ull, 0ull};
-#pragma unroll 1
-        for (int h = 1; h >= 0; --h) {
-          if (h == 0) scores(0);                         // (the second half is still there)
-          uint32_t pk[32];
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const uint64_t t =
-                fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, ref2);
-            float p0, p1;
-            unpack2(t, p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            ls[(c >> 1) & 1] = add2(ls[(c >> 1) & 1], pack2(p0, p1));
-            pk[c >> 1] = pack_bf16x2(p0, p1);
-          }
-          tmem_st32(tS + C::P_COL + h * 32, pk);         // over the second half of S
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(smem_u32(h ? &p_half[p] : &p_full[p]));
-        }
-        float l0, l1;
-        unpack2(add2(ls[0], ls[1]), l0, l1);
-        l += l0 + l1;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&p_full[p]));
       }
       if (!PAIR && p >= seg.n) mbar_arrive(smem_u32(&q_empty[0]));   // it had no block
-      // ---- the segment's result, one row a thread
+      // ---- the segment's result: half of a row's columns a thread
       const bool whole = seg.j0 == 0 && seg.n == seg.nb;
       const size_t prt = (size_t)blockIdx.x * 2 + (u == u0 ? 0 : 1);   // its slot
       const int pr = (PAIR ? p * 128 : 0) + r;
       const int t = seg.row0 + qi;
-      auto put = [&](int c0, const uint32_t* o, float f) {   // 32 columns
+      auto put = [&](int c0, const uint32_t* o, float f) {   // 32 columns, from c0 of this half on
         if (!live) return;
+        c0 += half * (DH / 2);
         if (whole) {
           bf16* const dst = (bf16*)a.out + t * a.os + hq * DH + c0;
 #pragma unroll
@@ -436,7 +428,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         }
       };
       auto stats = [&](float mm, float ll) {
-        if (!live) return;
+        if (!live || half) return;
         if (!whole) a.part_ml[prt * QT + pr] = make_float2(mm, ll);
         else if (a.lse)
           a.lse[(size_t)t * a.n_heads + hq] =
@@ -445,10 +437,14 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
       if (PAIR || p == 0 || seg.n > 1) (void)mbar_wait(smem_u32(&o_full[p]), oc++ & 1, abort);
       tc_fence_after();
       if (*abort) l = NAN;                              // a wait gave up: no result, and none to trust
+      *mine = l;
+      named_sync(rows_bar, 64);
+      l += *others;
+      named_sync(rows_bar, 64);                         // before the next maximum replaces it
       if constexpr (PAIR) {
         const float f = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
-        for (int c = 0; c < DH; c += 32) {
+        for (int c = 0; c < DH / 2; c += 32) {
           uint32_t o[32];
           tmem_ld32(tO + c, o);
           put(c, o, f);
@@ -458,23 +454,23 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         // pair 1's state goes to pair 0 through the second Q tile: (max, sum),
         // then half of O at a time, stored [column][row]
         float* buf = (float*)(sQ + C::TILE);
-        if (p == 1) ((float2*)buf)[r] = make_float2(m, l);
-        named_sync(3, 256);
+        if (p == 1 && half == 0) ((float2*)buf)[r] = make_float2(m, l);
+        named_sync(11, 512);
         const float2 o1 = ((const float2*)buf)[r];
-        named_sync(3, 256);
+        named_sync(11, 512);
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          if (p == 1 && seg.n > 1) {
+          if (p == 1 && half == h && seg.n > 1) {
 #pragma unroll 1
             for (int c = 0; c < DH / 2; c += 32) {
               uint32_t o[32];
-              tmem_ld32(tO + h * (DH / 2) + c, o);
+              tmem_ld32(tO + c, o);
 #pragma unroll
               for (int i = 0; i < 32; ++i) buf[(c + i) * 128 + r] = __uint_as_float(o[i]);
             }
           }
-          named_sync(3, 256);
-          if (p == 0) {
+          named_sync(11, 512);
+          if (p == 0 && half == h) {
             const float mm = fmaxf(m, o1.x), rf = mm == -INFINITY ? 0.f : mm;
             const float f0 = ex2(m - rf), f1 = seg.n > 1 ? ex2(o1.x - rf) : 0.f;
             const float ll = l * f0 + (seg.n > 1 ? o1.y * f1 : 0.f);
@@ -482,18 +478,18 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
 #pragma unroll 1
             for (int c = 0; c < DH / 2; c += 32) {
               uint32_t o[32];
-              tmem_ld32(tO + h * (DH / 2) + c, o);
+              tmem_ld32(tO + c, o);
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 float v = __uint_as_float(o[i]) * f0;
                 if (seg.n > 1) v = fmaf(buf[(c + i) * 128 + r], f1, v);
                 o[i] = __float_as_uint(v);
               }
-              put(h * (DH / 2) + c, o, f);
+              put(c, o, f);
             }
-            if (h == 0) stats(mm, ll);
+            stats(mm, ll);
           }
-          named_sync(3, 256);
+          named_sync(11, 512);
         }
       }
       tc_fence_before();
