@@ -38,10 +38,16 @@ struct CtCfg {
   static constexpr int BOX = 128 * 128;                // its 64-column half
   static constexpr int STAGES = DH == 128 ? 5 : 8;
   static constexpr int O_COL = 256;                    // TMEM: S0, S1 (128 each), O0, O1
-  static constexpr int P_COL = 64;                     // P over the second half of its S
-  static constexpr int BARS = 2 * STAGES + 10;         // full, empty; per pair s_full, p_full,
-                                                       //   o_full, q_full, q_empty
-  static constexpr int SMEM = 2 * TILE + STAGES * TILE + 4 * 128 * 4 + BARS * 8 + 16;
+  // Width 64 leaves TMEM columns for P of its own (after O), so a pair's next S
+  // is made while its exponentials run; at 128 P lies over the second half of S,
+  // and the next S follows the PV that reads it.  (At 128, S in two halves of 64
+  // keys, the first made early, was slower: 8,192 rows under a 2,048 window 286
+  // -> 307 us, as the queries are read from shared memory twice.)
+  static constexpr bool AHEAD = DH == 64;
+  static constexpr int P_COL = AHEAD ? O_COL + 64 : 64;   // of pair 0; pair 1: 128 on
+  static constexpr int BARS = 2 * STAGES + 12;         // full, empty; per pair s_full, s_read,
+                                                       //   p_full, o_full, q_full, q_empty
+  static constexpr int SMEM = 2 * TILE + STAGES * TILE + 4 * 128 * 4 + BARS * 8 + 16 * 4 + 16;
 };
 
 // A stretch of one tile's units inside a CTA's run: nv of them, of which the
@@ -91,9 +97,12 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
   // positions of a pair's block lie over its first half's
   float* s_mx = (float*)(sKV + C::STAGES * C::TILE);
   uint64_t* bars = (uint64_t*)(s_mx + 512);
-  uint64_t *full = bars, *empty = bars + C::STAGES, *s_full = empty + C::STAGES, *p_full = s_full + 2,
-           *o_full = p_full + 2, *q_full = o_full + 2, *q_empty = q_full + 2;
-  uint32_t* tmem_slot = (uint32_t*)(bars + C::BARS);
+  uint64_t *full = bars, *empty = bars + C::STAGES, *s_full = empty + C::STAGES, *s_read = s_full + 2,
+           *p_full = s_read + 2,           *o_full = p_full + 2, *q_full = o_full + 2, *q_empty = q_full + 2;
+  // pages of a block that exist, by block of the CTA: written before its keys
+  // are asked for, and at most STAGES / 2 + 1 blocks before its values are used
+  uint32_t* s_pages = (uint32_t*)(bars + C::BARS);     // [16]
+  uint32_t* tmem_slot = s_pages + 16;
   volatile int* abort = (volatile int*)(tmem_slot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
@@ -105,6 +114,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&p_full[i]), 256);
+      mbar_init(smem_u32(&s_read[i]), 256);
       mbar_init(smem_u32(&o_full[i]), 1);
       mbar_init(smem_u32(&q_full[i]), 1);
       mbar_init(smem_u32(&q_empty[i]), PAIR ? 256 : 512);
@@ -159,6 +169,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
           const int page = cache_page(a.c, seg.b, r);
           if (page >= 0) row = (page * a.c.n_kv + seg.g) << a.c.ps_log2;
         }
+        const uint32_t pages = __ballot_sync(0xffffffffu, row != gone);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++cnt) {
           const int st = cnt % C::STAGES;
@@ -166,7 +177,10 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
           go = __all_sync(0xffffffffu, ok);
           if (!go) continue;
           const uint32_t fb = smem_u32(&full[st]);
-          if (lane == 0) mbar_expect_tx(fb, C::TILE);
+          if (lane == 0) {
+            if (kv == 0) s_pages[(cnt >> 1) & 15] = pages;
+            mbar_expect_tx(fb, C::TILE);
+          }
           __syncwarp();
           if (lane < np)
 #pragma unroll
@@ -180,8 +194,9 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer.  Step s of a segment: PAIR: block s/2 for
-    // pair s%2; else block s for pair s%2.  S runs two steps ahead of PV, and
-    // S of a pair is issued after the PV that reads the P it overwrites.
+    // pair s%2; else block s for pair s%2.  S runs two steps ahead of PV: a
+    // pair's next S is issued once its scores have been read (AHEAD), else
+    // after the PV that reads the P it overwrites.
     constexpr uint32_t idS = idesc_bf16<128>();
     constexpr uint32_t idO = idesc_bf16<DH>() | (1u << 16);   // V: MN-major
     // a wait that gave up is not acted on here: the remaining products run on
@@ -189,7 +204,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     const uint64_t dk = desc_sw128(smem_u32(sKV)), dq = desc_sw128(smem_u32(sQ)),
                    dv = desc_sw128_mn(smem_u32(sKV), C::BOX);
     int cnt = 0, nseg = 0;                              // ring entries of earlier segments
-    uint32_t pc0 = 0, pc1 = 0;
+    uint32_t pc0 = 0, pc1 = 0;                          // PV steps of each pair so far
     for (int u = u0; u < u1; u += seg.nv, ++nseg) {
       seg.at(a, u, u1);
       if (seg.n == 0) break;
@@ -211,23 +226,30 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
       auto issue_pv = [&](int s) {
         const int j = PAIR ? s >> 1 : s, p = s & 1;
         const int c = cnt + 2 * j + 1, st = c % C::STAGES;
-        const uint32_t ph = (p ? pc1++ : pc0++) & 1;
         (void)mbar_wait(smem_u32(&full[st]), (c / C::STAGES) & 1, abort);
-        (void)mbar_wait(smem_u32(&p_full[p]), ph, abort);
+        (void)mbar_wait(smem_u32(&p_full[p]), (p ? pc1 : pc0) & 1, abort);
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          tc_mma4_ts(tmem + C::O_COL + p * 128, tmem + p * 128 + C::P_COL + h * 32,
+          tc_mma4_ts(tmem + C::O_COL + p * 128, tmem + C::P_COL + p * 128 + h * 32,
                      (uint32_t)dv + ((st * C::TILE + h * 64 * 128) >> 4), (uint32_t)(dv >> 32), idO,
                      s >= 2 || h > 0);
         if (!PAIR || p == 1) tc_commit_elect(smem_u32(&empty[st]));
-        if (s + 2 >= steps) tc_commit_elect(smem_u32(&o_full[p]));
+        if (C::AHEAD || s + 2 >= steps) tc_commit_elect(smem_u32(&o_full[p]));
       };
       issue_s(0);
       if (steps > 1) issue_s(1);
       for (int s = 0; s < steps; ++s) {
+        const int p = s & 1;
+        const bool more = s + 2 < steps;
+        if (C::AHEAD && more) {
+          // (a pair's s_read and p_full complete once a step, so they share the count)
+          (void)mbar_wait(smem_u32(&s_read[p]), (p ? pc1 : pc0) & 1, abort);
+          issue_s(s + 2);
+        }
         issue_pv(s);
-        if (s + 2 < steps) issue_s(s + 2);
+        if (!C::AHEAD && more) issue_s(s + 2);
+        p ? ++pc1 : ++pc0;
       }
       cnt += 2 * n;
       seg.done(a);
@@ -245,7 +267,8 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     // ---------------- softmax: thread = 64 keys (`half`) of packed row `r` of pair `p`
     const int p = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, r = tid & 127;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tS = tl + p * 128, tO = tl + C::O_COL + p * 128 + half * (DH / 2);
+    const uint32_t tS = tl + p * 128, tO = tl + C::O_COL + p * 128 + half * (DH / 2),
+                   tP = tl + C::P_COL + p * 128 + half * 32;
     const int rows_bar = 1 + p * 4 + (warp & 3), pair_bar = 9 + p;   // two warps, eight warps
     float* const mine = s_mx + (p * 2 + half) * 128 + r;
     const float* const others = s_mx + (p * 2 + (half ^ 1)) * 128 + r;
@@ -264,28 +287,36 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
       const bool live = r < a.rt && x < all;
       const int qi = live ? x / a.G : 0, hq = seg.g * a.G + (live ? x - qi * a.G : 0);
       const int pq = a.q_pos ? __ldg(a.q_pos + seg.row0 + qi) : seg.p0 + qi;
-      // positions that every row of this pair sees: [.., pmin], window from pmax
-      const int pmin = seg.p0 + min(xw, all - 1) / a.G;
-      const int pmax = seg.p0 + (min(xw + a.rt, all) - 1) / a.G;
+      // blocks that every row of this pair sees whole: those from row `open_lo` to
+      // row `open_hi` on (p_first, p_last: the pair's first and last position)
+      const int p_first = seg.p0 + min(xw, all - 1) / a.G;
+      const int p_last = seg.p0 + (min(xw + a.rt, all) - 1) / a.G;
+      const int open_lo = max(seg.seen.lo, a.window > 0 ? p_last - a.window + 1 : 0);
+      const int open_hi = a.c.pos ? -1 : min(seg.seen.hi - CT_KB, p_first - (CT_KB - 1));
       float m = -INFINITY, l = 0.f;                     // l: this thread's keys
       bool first = true;
-      // lane's page-table entry of a block, loaded one block before it is looked at
-      auto page_of = [&](int j) {
-        const int i = (blocks.row(seg.j0 + j) >> a.c.ps_log2) + lane;
-        return lane < np && j < seg.n && i < a.c.table_stride
-                   ? __ldg(a.c.table + (size_t)seg.b * a.c.table_stride + i) : -1;
-      };
-      int page = page_of(PAIR ? 0 : p);
       for (int j = PAIR ? 0 : p; j < seg.n; j += PAIR ? 1 : 2) {
         const int r0 = blocks.row(seg.j0 + j);
-        const uint32_t pages = __ballot_sync(0xffffffffu, (unsigned)page < (unsigned)a.c.n_pages);
-        page = page_of(j + (PAIR ? 1 : 2));
-        const bool inside = r0 >= seg.seen.lo && r0 + CT_KB <= seg.seen.hi;
-        const bool open = !a.c.pos && inside && pages == all_pages && r0 + CT_KB - 1 <= pmin &&
-                          (a.window == 0 || pmax - r0 < a.window);
+        // The scores or the V tile say that the block's pages are noted down.  The
+        // V tile where it is there already as a rule and this thread, waiting for
+        // the scores, can decide about masks meanwhile (8,192 rows under a 2,048
+        // window, width 128: 283 us against 292).  The scores where the loop is
+        // bound by this thread's instructions (width 64, 8,192 causal rows: 376 us
+        // against 396) or by the tiles' arrival (one Q tile).
+        const int ring = cnt + 2 * j + 1;               // the block's V tile
+        auto wait_v = [&]() {
+          (void)mbar_wait(smem_u32(&full[ring % C::STAGES]), (ring / C::STAGES) & 1, abort);
+        };
+        auto wait_s = [&]() { (void)mbar_wait(smem_u32(&s_full[p]), sc++ & 1, abort); };
+        constexpr bool BY_V = PAIR && !C::AHEAD;
+        if constexpr (BY_V) wait_v();
+        else wait_s();
+        const uint32_t pages = s_pages[(ring >> 1) & 15];
+        const bool open = r0 >= open_lo && r0 <= open_hi && pages == all_pages;
         uint32_t see0 = ~0u, see1 = ~0u;                // this thread's mask of its 64 keys
         if (!open) {
           const int kr = r0 + r;
+          const bool inside = r0 >= seg.seen.lo && r0 + CT_KB <= seg.seen.hi;
           if (!inside || a.c.pos) {
             named_sync(pair_bar, 256);                  // the last block's readers are done
             if (a.c.pos && half == 0) {
@@ -297,8 +328,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             // value rows in pages that exist but that nobody sees may hold
             // anything: zero them, as 0 x NaN would not be 0
             if (!inside) {
-              const int ring = cnt + 2 * j + 1;         // the block's V tile
-              (void)mbar_wait(smem_u32(&full[ring % C::STAGES]), (ring / C::STAGES) & 1, abort);
+              if constexpr (!BY_V) wait_v();
               if (!row_seen(seg.seen, kr)) {
                 uint8_t* v = sKV + (ring % C::STAGES) * C::TILE + r * 128;
 #pragma unroll
@@ -335,8 +365,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
           see0 = (uint32_t)see & k0;
           see1 = (uint32_t)(see >> 32) & k1;
         }
-        (void)mbar_wait(smem_u32(&s_full[p]), sc & 1, abort);
-        ++sc;
+        if constexpr (BY_V) wait_s();
         // the tile's last scores are there: its queries may be replaced
         if (j + (PAIR ? 1 : 2) >= seg.n) mbar_arrive(smem_u32(&q_empty[PAIR ? p : 0]));
         tc_fence_after();
@@ -347,16 +376,20 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
           for (int c = 0; c < 64; ++c)
             if (!(((c < 32 ? see0 : see1) >> (c & 31)) & 1u)) s[c] = 0xff800000u;   // -inf
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mx[2] = {__uint_as_float(s[0]), __uint_as_float(s[1])};
 #pragma unroll
-        for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
-        const float my_top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int c = 2; c < 62; c += 4)
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            mx[z] = max3(mx[z], __uint_as_float(s[c + 2 * z]), __uint_as_float(s[c + 2 * z + 1]));
+        const float my_top = max3(fmaxf(mx[0], mx[1]), __uint_as_float(s[62]), __uint_as_float(s[63]));
         *mine = my_top;
         // also: both halves of the scores are in registers, P may overwrite them
         tc_fence_before();
         named_sync(rows_bar, 64);
         tc_fence_after();
         const float top = fmaxf(my_top, *others) * a.scale_log2;
+        if (C::AHEAD) mbar_arrive(smem_u32(&s_read[p]));
         // (both halves of a row come to the same m and f)
         const bool grow = !first && __any_sync(0xffffffffu, top > m + 8.f);
         float f = 1.f;
@@ -368,7 +401,6 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
           m = mn;
           l *= f;
         }
-        first = false;
         const float ref = m == -INFINITY ? 0.f : m;
         const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
         uint64_t ls[2] = {0ull, 0ull};
@@ -383,7 +415,12 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
           ls[(c >> 1) & 1] = add2(ls[(c >> 1) & 1], pack2(p0, p1));
           s[c >> 1] = pack_bf16x2(p0, p1);
         }
-        tmem_st32(tS + C::P_COL + half * 32, s);         // over the second half of S
+        if (C::AHEAD && !first) {                        // the PV before has read P and left O alone
+          (void)mbar_wait(smem_u32(&o_full[p]), oc++ & 1, abort);
+          tc_fence_after();
+        }
+        first = false;
+        tmem_st32(tP, s);
         float l0, l1;
         unpack2(add2(ls[0], ls[1]), l0, l1);
         l += l0 + l1;
@@ -451,45 +488,41 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         }
         stats(m, l);
       } else {
-        // pair 1's state goes to pair 0 through the second Q tile: (max, sum),
-        // then half of O at a time, stored [column][row]
-        float* buf = (float*)(sQ + C::TILE);
-        if (p == 1 && half == 0) ((float2*)buf)[r] = make_float2(m, l);
-        named_sync(11, 512);
-        const float2 o1 = ((const float2*)buf)[r];
-        named_sync(11, 512);
+        // pair 1's state goes to pair 0: (max, sum) in its two slots of s_mx, O
+        // through the second Q tile (64 columns at width 128, 32 at 64) in two
+        // rounds; the four warps of a row meet
+        const int merge_bar = 11 + (warp & 3);
+        if (p == 1) *mine = half ? l : m;
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          if (p == 1 && half == h && seg.n > 1) {
-#pragma unroll 1
-            for (int c = 0; c < DH / 2; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(tO + c, o);
+        for (int k = 0; k < 2; ++k) {
+          const bool on = DH == 128 || half == k;
+          const int c = DH == 128 ? 32 * k : 0;
+          float* const buf = (float*)(sQ + C::TILE) + (DH == 128 ? half * 32 * 128 : 0) + r;
+          if (p == 1 && on && seg.n > 1) {
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) buf[(c + i) * 128 + r] = __uint_as_float(o[i]);
-            }
+            for (int i = 0; i < 32; ++i) buf[i * 128] = __uint_as_float(o[i]);
           }
-          named_sync(11, 512);
-          if (p == 0 && half == h) {
-            const float mm = fmaxf(m, o1.x), rf = mm == -INFINITY ? 0.f : mm;
-            const float f0 = ex2(m - rf), f1 = seg.n > 1 ? ex2(o1.x - rf) : 0.f;
-            const float ll = l * f0 + (seg.n > 1 ? o1.y * f1 : 0.f);
+          named_sync(merge_bar, 128);
+          if (p == 0 && on) {
+            const float m1 = s_mx[256 + r], l1 = s_mx[384 + r];
+            const float mm = fmaxf(m, m1), rf = mm == -INFINITY ? 0.f : mm;
+            const float f0 = ex2(m - rf), f1 = seg.n > 1 ? ex2(m1 - rf) : 0.f;
+            const float ll = l * f0 + (seg.n > 1 ? l1 * f1 : 0.f);
             const float f = ll != 0.f ? 1.f / ll : 0.f;
-#pragma unroll 1
-            for (int c = 0; c < DH / 2; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(tO + c, o);
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                float v = __uint_as_float(o[i]) * f0;
-                if (seg.n > 1) v = fmaf(buf[(c + i) * 128 + r], f1, v);
-                o[i] = __float_as_uint(v);
-              }
-              put(c, o, f);
+            for (int i = 0; i < 32; ++i) {
+              float v = __uint_as_float(o[i]) * f0;
+              if (seg.n > 1) v = fmaf(buf[i * 128], f1, v);
+              o[i] = __float_as_uint(v);
             }
-            stats(mm, ll);
+            put(c, o, f);
+            if (k == 0) stats(mm, ll);
           }
-          named_sync(11, 512);
+          named_sync(merge_bar, 128);
         }
       }
       tc_fence_before();
