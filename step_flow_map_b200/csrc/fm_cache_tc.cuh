@@ -2,20 +2,24 @@
 // rows per key/value head: drafted blocks, prompts) on tcgen05.
 //
 // Per block of 128 cache rows: S = Q K^T (128 packed rows x 128 keys, fp32 in
-// TMEM), P = 2^(S - m) rounded to bf16 over the second half of S, O += P V with P
-// read from TMEM.  Keys and values come page by page through TMA into a ring
+// TMEM), P = 2^(S - m) rounded to bf16 (the tensor path's type; the sums take p
+// as it is), O += P V with P read from TMEM.  Keys and values come page by page through TMA into a ring
 // of 128-row tiles (128-byte swizzle): K as the K-major operand, V as it lies,
 // MN-major.  Two S/O pairs fill TMEM (2 x (128 + DH) columns), so one's
 // exponentials run under the other's products; two softmax warpgroups work on
-// each, a thread on 64 keys of one packed row (with one warpgroup per pair, a
-// thread on all 128 keys, the chain of loads, maximum, exponentials and stores
-// was 2,900 of a block's 3,900 clocks):
+// each, a thread on 64 keys of one packed row (one warpgroup per pair, a thread
+// on all 128 keys: 75 us for 2,777 rows over 4,001, 16 heads of width 64,
+// against 68):
 //   PAIR  (more than 128 packed rows) the pairs are two tiles of 128 rows that
 //         share every K/V tile;
 //   else  one tile of 128 rows: even blocks go to pair 0, odd ones to pair 1,
 //         merged at the end of the tile.
-// Bound: for prompts the exponentials (16 a clock and SM) and the products
-// about equally; for drafted blocks HBM.
+// Bound: for prompts the exponentials (16 a clock and SM) and the products, each
+// 43-44 % busy at width 128, where a pair's next S waits for the PV that reads
+// its P; for drafted blocks HBM.  Measured: 8,192 rows, 32 heads of width 128,
+// causal 1.0-1.08 PFLOP/s, under a 2,048 window 317 us (0.76); 2,777 rows over
+// 4,001, width 64, 61 us (0.48); 48 blocks of 17 rows over 2,048..4,096: 135 us
+// with plan and join, 5.6 TB/s inside the kernel.
 //
 // Roles (640 threads): warp 0 TMA, warp 1 MMA, warps 4-19 softmax.
 // O is rescaled by the softmax threads, and only when a row maximum has grown
