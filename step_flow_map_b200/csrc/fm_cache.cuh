@@ -293,7 +293,9 @@ __global__ void __launch_bounds__(CA_THREADS, 3) k_cache_append(const AppendArgs
 // at once.
 //
 // Bound: the latency of the passes for few rows (each a few shared-memory
-// round trips and a barrier); 8 bytes per row plus the moved rows beyond that.
+// round trips and a barrier: 256 pairs of 1,041 rows 15 us); 8 bytes per row
+// plus the moved rows beyond that (64 pairs of up to 16,384 rows cut to 2,048:
+// 47 us, of which 22 move the rows at 4.7 TB/s).
 constexpr int EV_THREADS = 512;
 constexpr int EV_SLICE = 32768;    // most rows of one CTA (64 steps of a warp: one flag word)
 constexpr int EV_MAX_CLUSTER = 8;

@@ -295,7 +295,7 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
       // row `open_hi` on (p_first, p_last: the pair's first and last position)
       const int p_first = seg.p0 + min(xw, all - 1) / a.G;
       const int p_last = seg.p0 + (min(xw + a.rt, all) - 1) / a.G;
-      const int open_lo = max(seg.seen.lo, a.window > 0 ? p_last - a.window + 1 : 0);
+      const int open_lo = max(seg.seen.lo, a.window > 0 && p_last >= a.window ? p_last - a.window + 1 : 0);
       const int open_hi = a.c.pos ? -1 : min(seg.seen.hi - CT_KB, p_first - (CT_KB - 1));
       float m = -INFINITY, l = 0.f;                     // l: this thread's keys
       bool first = true;

@@ -81,7 +81,7 @@ def cu_of(rows):
 
 
 def check_attention(w, rows, G, window=0, sinks=0, q_pos=None, accumulate=False, tail=2, max_rows=None,
-                    there=None, sharp=1.0, strided=False, run=None):
+                    there=None, sharp=1.0, strided=False, run=None, max_kv=None):
     hq, dh, T = w.hkv * G, w.dh, sum(rows)
     q = torch.tensor(w.rng.normal(size=(T + tail, hq, dh)) * sharp).to(DT[w.dtype]).cuda()
     out = torch.full((T + tail, hq, dh), 77.0, dtype=DT[w.dtype]).cuda()
@@ -94,7 +94,7 @@ def check_attention(w, rows, G, window=0, sinks=0, q_pos=None, accumulate=False,
     if q_pos is not None:
         pq = torch.tensor(np.concatenate([q_pos, np.zeros(tail)]), dtype=torch.int32).cuda()
     before = w.weight.clone() if w.weight is not None else None
-    args = dict(max_rows=max_rows or max(1, max(rows)), max_kv=max(1, max(w.lens)), q_pos=pq, window=window,
+    args = dict(max_rows=max_rows or max(1, max(rows)), max_kv=max_kv or max(1, max(w.lens)), q_pos=pq, window=window,
                 sinks=sinks, accumulate=accumulate, lse=True, out=out)
     got, lse = (run or (lambda: w.cache.attend(q, cu_of(rows), w.kv, **args)))()
     again, lse2 = w.cache.attend(q, cu_of(rows), w.kv, **{**args, "accumulate": False, "out": torch.empty_like(out)})
@@ -505,3 +505,37 @@ def test_a_stream_of_another_kind_of_handle():
     b = w.cache.attend(q, cu_of([3]), w.kv, max_rows=3, max_kv=90, stream=side.cuda_stream)
     side.synchronize()
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 17, 150])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
+def test_stored_positions_decide_at_width_128(dtype, rows, window, sinks):
+    """Positions far apart, in any order, over caches of several blocks."""
+    lens = [500, 155, 160]
+    w = World(lens, 2, 128, 32, dtype, seed=rows, pos=True)
+    for b, L in enumerate(lens):
+        w.put(w.pos, b, torch.tensor(np.stack([w.rng.permutation(L) * (b + 1) for _ in range(2)], 1)))
+    q_pos = np.concatenate([np.sort(w.rng.integers(0, L * (b + 1), rows)) for b, L in enumerate(lens)])
+    check_attention(w, [rows] * 3, 4, window, sinks, q_pos=q_pos)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 17, 140])
+@pytest.mark.parametrize("max_kv", [1, 100, 129])
+def test_a_sequence_longer_than_max_kv_is_cut(dtype, rows, max_kv):
+    """Its rows keep their positions; the cached rows from max_kv on are not read."""
+    w = World([300, 60, 128], 2, 64, 16, dtype, seed=max_kv, weight=True)
+    n = [rows, min(rows, 60), min(rows, 128)]
+    there = [np.arange(L) < max_kv for L in w.lens]
+    check_attention(w, n, 4, 0, 0, there=there, max_kv=max_kv, accumulate=True)
+    check_attention(w, n, 4, 250, 2, there=there, max_kv=max_kv)
+
+
+@pytest.mark.parametrize("dtype,dh", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("rows", [1, 40, 200])
+def test_largest_window_and_sinks(dtype, dh, rows):
+    """The largest numbers mean no window at all, also before row 0."""
+    w = World([7, 0, 64, 300], 1, dh, 16, dtype)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (5, 2 ** 31 - 1)):
+        check_attention(w, [rows + 7, rows, 64, rows], 8, window, sinks)
