@@ -8,7 +8,8 @@
 // round trip per 16 keys).  fp32: FMAs, two lanes per key for the scores and
 // DH / 32 columns a lane for the output, four rows at a time, so that few rows
 // cost few instructions.  Measured: one token over 131,071 rows of 8 heads of
-// width 128 in bf16 104 us, 5.2 TB/s; 8 tokens over 3,000 rows of 4 heads of
+// width 128 in bf16 97 us with the join (107 when both cursors worked out their
+// rows anew for every unit), 64 tokens with weights 167 us (186); 8 tokens over 3,000 rows of 4 heads of
 // width 64 in fp32 24 us with the join (108 in tiles of the prompt kernel).  A unit is 64 cache rows of one (sequence, head); each of
 // the four warps owns 16 of them and its own three-stage cp.async ring (16
 // rows of a head are one contiguous block of a page), so the loop has no CTA
@@ -80,25 +81,42 @@ __device__ __forceinline__ int decode_find(const CacheAttnArgs& a, const DecodeS
   return b;
 }
 
-// A unit of the CTA's run: block j of head g of sequence b.
+// A unit of the CTA's run, block j of head g of sequence b, and the first of
+// this warp's 16 rows in it; stepping on is an addition but where the sequence
+// changes.
 struct DecodeCursor {
-  int b, g, j, nb;
+  int b, g, j, nb, row;
+  int ns, main;                    // blocks of [0, s_end); this warp's row of the first one past them
+  SeenRows v;
+  __device__ __forceinline__ void open(const CacheAttnArgs& a, const DecodeSeqs& s) {
+    v = s.seen(a, b);
+    const SeenBlocks<CD_KB> k(v);
+    ns = k.ns;
+    main = k.b0 * CD_KB + 16 * (threadIdx.x >> 5);
+  }
   __device__ __forceinline__ void seek(const CacheAttnArgs& a, const DecodeSeqs& s, int u) {
     b = decode_find(a, s, u);
     nb = s.first[b + 1] - s.first[b];
+    open(a, s);
     const int at = u - s.first[b] * a.c.n_kv;
     g = at / nb;
     j = at - g * nb;
+    row = j < ns ? j * CD_KB + 16 * (threadIdx.x >> 5) : (j - ns) * CD_KB + main;
   }
   __device__ __forceinline__ void next(const CacheAttnArgs& a, const DecodeSeqs& s) {
-    if (++j < nb) return;
+    row += CD_KB;
+    if (++j == ns) row = main;
+    if (j < nb) return;
     j = 0;
-    if (++g < a.c.n_kv) return;
-    g = 0;
-    do {
-      ++b;
-      nb = b < 256 ? s.first[b + 1] - s.first[b] : 1;
-    } while (nb == 0);
+    if (++g == a.c.n_kv) {
+      g = 0;
+      do {
+        ++b;                       // (there is a next unit, so there is a next sequence)
+        nb = s.first[b + 1] - s.first[b];
+      } while (nb == 0);
+      open(a, s);
+    }
+    row = ns > 0 ? 16 * (threadIdx.x >> 5) : main;
   }
 };
 
@@ -412,33 +430,30 @@ __global__ void __launch_bounds__(CD_THREADS, (CdCfg<T, DH>::CTAS)) k_cache_deco
   cu = ld;
   if (tid == 0)
     put_join(a, w, blockIdx.x, u0 - ld.j, ld.nb, s.row0[ld.b], ld.g, 0, s.n[ld.b] * a.G);
-  auto tile_row = [&](const DecodeCursor& c) {
-    const SeenRows v = s.seen(a, c.b);
-    return SeenBlocks<CD_KB>(v).row(c.j) + 16 * warp;
-  };
-  int ld_row = tile_row(ld), ld_page = cache_page(a.c, ld.b, ld_row);
-  // stage `st` <- the load cursor's unit; then the cursor moves on and its
-  // page number starts loading
-  auto load = [&](int st, bool more) {
-    const SeenRows v = s.seen(a, ld.b);
+  int ld_page = cache_page(a.c, ld.b, ld.row);
+  uint32_t there = 0;              // bit k % 32: the page of the run's unit k exists
+  // stage `st` <- the load cursor's unit, the run's unit k; then the cursor moves
+  // on and its page number starts loading
+  auto load = [&](int st, int k, bool more) {
     const uint32_t dst = ring + st * C::STAGE;
-    const size_t at = cache_row(a.c, max(ld_page, 0), ld.g, ld_row);
-    const char* gk = (const char*)a.c.k + at * C::ROW;
-    const char* gv = (const char*)a.c.v + at * C::ROW;
+    const size_t at = cache_row(a.c, max(ld_page, 0), ld.g, ld.row);
+    const char* gk = (const char*)a.c.k + at * C::ROW + lane * 16;
+    const char* gv = (const char*)a.c.v + at * C::ROW + lane * 16;
+    there = (there & ~(1u << (k & 31))) | (uint32_t)(ld_page >= 0) << (k & 31);
+    const bool all = ld_page >= 0 && ld.row >= ld.v.lo && ld.row + 16 <= ld.v.hi;
 #pragma unroll
     for (int i = 0; i < CH / 2; ++i) {
       const int x = lane + 32 * i, r = x / CH, c = x % CH;
-      const bool live = ld_page >= 0 && row_seen(v, ld_row + r);
+      const bool live = all || (ld_page >= 0 && row_seen(ld.v, ld.row + r));
       const uint32_t o = r * C::ROW + ((c ^ (r & 7)) << 4);
-      cp_async16_if(dst + o, gk + x * 16, live);
-      cp_async16_if(dst + C::TILE + o, gv + x * 16, live);
+      cp_async16_if(dst + o, gk + i * 512, live);
+      cp_async16_if(dst + C::TILE + o, gv + i * 512, live);
     }
     if (a.c.pos && lane < 4)
       cp_async16_if(dst + 2 * C::TILE + lane * 16, a.c.pos + at + lane * 4, ld_page >= 0);
     if (more) {
       ld.next(a, s);
-      ld_row = tile_row(ld);
-      ld_page = cache_page(a.c, ld.b, ld_row);
+      ld_page = cache_page(a.c, ld.b, ld.row);
     }
   };
   int issued = 0;
@@ -446,11 +461,10 @@ __global__ void __launch_bounds__(CD_THREADS, (CdCfg<T, DH>::CTAS)) k_cache_deco
   for (int i = 0; i < CD_STAGES - 1; ++i) {
     if (issued < count) {
       ++issued;
-      load(i, issued < count);
+      load(i, i, issued < count);
     }
     cp_commit();
   }
-  int cu_page = cache_page(a.c, cu.b, tile_row(cu));
 
   int done = 0, stage = 0;
   while (done < count) {
@@ -458,7 +472,7 @@ __global__ void __launch_bounds__(CD_THREADS, (CdCfg<T, DH>::CTAS)) k_cache_deco
     const int b = cu.b, g = cu.g, j0 = cu.j, nb = cu.nb;
     const int todo = min(nb - j0, count - done);
     const int rows = s.n[b] * a.G, row0 = s.row0[b], p0 = s.len[b];
-    const SeenRows seen = s.seen(a, b);
+    const SeenRows seen = cu.v;
     const DecodeTile tile = {rows, row0, p0, p0 + s.n[b] - 1, g, seen};
     DecodeState<T, DH> state;
     state.begin(a, tile, sq);
@@ -471,19 +485,16 @@ __global__ void __launch_bounds__(CD_THREADS, (CdCfg<T, DH>::CTAS)) k_cache_deco
         const int st = stage == 0 ? CD_STAGES - 1 : stage - 1;
         if (issued < count) {
           ++issued;
-          load(st, issued < count);
+          load(st, issued - 1, issued < count);
         }
         cp_commit();
       }
-      const int r0 = tile_row(cu);
-      const bool there = cu_page >= 0;
-      if (it + 1 < todo) {
-        cu.next(a, s);
-        cu_page = cache_page(a.c, cu.b, tile_row(cu));
-      }
+      const int r0 = cu.row;
+      const bool here = there >> ((done + it) & 31) & 1u;
+      if (it + 1 < todo) cu.next(a, s);
       const uint32_t kt = ring + stage * C::STAGE;
       // nothing of the tile is visible: skip it
-      if (there && (r0 < seen.s_end || (r0 + 16 > seen.lo && r0 < seen.hi))) {
+      if (here && (r0 < seen.s_end || (r0 + 16 > seen.lo && r0 < seen.hi))) {
         const DecodeKeys keys = {
             kt, kt + C::TILE, (const int*)(smb + warp * C::RING + stage * C::STAGE + 2 * C::TILE), r0,
             a.scores ? a.scores + score_at(a, b, g, r0, 0) : nullptr,
@@ -545,10 +556,7 @@ __global__ void __launch_bounds__(CD_THREADS, (CdCfg<T, DH>::CTAS)) k_cache_deco
     }
     __syncthreads();               // s_ml and the buffer are free again
     done += todo;
-    if (done < count) {
-      cu.next(a, s);
-      cu_page = cache_page(a.c, cu.b, tile_row(cu));
-    }
+    if (done < count) cu.next(a, s);
   }
   cp_wait<0>();
 }
