@@ -394,8 +394,10 @@ k_cache_attn_tc(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         tc_fence_after();
         const float top = fmaxf(my_top, *others) * a.scale_log2;
         if (C::AHEAD) mbar_arrive(smem_u32(&s_read[p]));
-        // (both halves of a row come to the same m and f)
-        const bool grow = !first && __any_sync(0xffffffffu, top > m + 8.f);
+        // (both halves of a row come to the same m and f; rows of no query, whose
+        // scores are of whatever the tile held or of the next sequence's queries,
+        // have no vote, so they cannot change how the others are rounded)
+        const bool grow = !first && __any_sync(0xffffffffu, live && top > m + 8.f);
         float f = 1.f;
         if (first) {
           m = top;
