@@ -324,7 +324,8 @@ typedef struct {
  *                dtype, `*_stride` elements apart (a multiple of 16 bytes), so
  *                the three may be slices of one projection's output
  *   q_gain, k_gain  device [head_dim] dtype: per head x / sqrt(mean(x^2) +
- *                eps) * gain; NULL leaves the heads as they are
+ *                eps) * gain; NULL leaves the heads as they are (infinities too;
+ *                a NaN stays one), as values past rot_dim are not turned
  *   inv_freq     device fp64 [rot_dim / 2]: pair i of a head's first rot_dim
  *                values turns by the angle position * inv_freq[i] (reduced in
  *                fp64, so far positions keep their angles); NULL with rot_dim
