@@ -121,7 +121,10 @@ class PagedCache:
     Calls run on `stream`, or on the current stream of the cache's device;
     outputs and workspaces are allocated on that stream, one workspace per
     call, so calls on different streams (or captured in different graphs)
-    share nothing but what they are given.
+    share nothing but what they are given.  Given `stream`, a call keeps the
+    allocator from handing out the memory of its tensors again, the cache's
+    included, before that stream is done with them, so that they may be
+    dropped at once; that they are written before it begins is up to the caller.
     """
 
     def __init__(self, k, v, page_table, pos=None, weight=None):
@@ -185,9 +188,10 @@ class PagedCache:
             self._check("q_pos", q_pos, torch.int32, (T,))
         return B
 
-    def _on(self, stream):
+    def _on(self, stream, *lent):
         """A context under which tensors are allocated on the cache's device and on
-        `stream` (None: the device's current stream), and that stream."""
+        `stream` (None: the device's current stream), and that stream, to which the
+        tensors `lent` (None among them) and the cache's are lent."""
         if self.device.type != "cuda":
             raise ValueError(f"the cache is on {self.device}; its operators run on a GPU")
         if stream is None:   # (the public accessors cost 5 us, as much as a small call's kernels)
@@ -198,6 +202,9 @@ class PagedCache:
             stream = torch.cuda.ExternalStream(stream, device=self.device)
         elif stream.device != self.device:
             raise ValueError(f"stream of {stream.device}, cache on {self.device}")
+        for t in (self.k, self.v, self.pos, self.weight, self._table, *lent):
+            if t is not None:
+                t.record_stream(stream)
         return torch.cuda.stream(stream), stream.cuda_stream
 
     def append(self, q, k, v, cu_rows, kv_len, q_pos=None, *, q_gain=None, k_gain=None, eps=1e-6,
@@ -217,7 +224,7 @@ class PagedCache:
         if inv_freq is not None:
             rot = 2 * inv_freq.shape[0]
             self._check("inv_freq", inv_freq, torch.float64, (rot // 2,))
-        ctx, st = self._on(stream)
+        ctx, st = self._on(stream, q, k, v, cu_rows, kv_len, q_pos, q_gain, k_gain, inv_freq, out)
         with ctx:
             if out is None:
                 out = q.new_empty(T, n_heads, dh)
@@ -240,7 +247,7 @@ class PagedCache:
         T, n_heads, dh = q.shape
         qs = self._rows("q", q, T, n_heads)
         B = self._seqs(T, cu_rows, kv_len, q_pos)
-        ctx, st = self._on(stream)
+        ctx, st = self._on(stream, q, cu_rows, kv_len, q_pos, out)
         with ctx:
             if out is None:
                 out = q.new_empty(T, n_heads, dh)
@@ -270,7 +277,7 @@ class PagedCache:
         self._check("next_pos", next_pos, torch.int32, (B,))
         if B > self._table.shape[0]:
             raise ValueError(f"{B} sequences, {self._table.shape[0]} rows of page_table")
-        ctx, st = self._on(stream)
+        ctx, st = self._on(stream, kv_len, next_pos, new_len)
         with ctx:
             if new_len is None:
                 new_len = kv_len.new_empty(B)
