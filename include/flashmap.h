@@ -299,7 +299,8 @@ fm_status fm_verify_greedy_noalloc(const float *target_logits, const int32_t *dr
  *                outside [0, n_pages) does not exist: nothing is written to
  *                it and no query sees it.
  * page_size is 16, 32, 64 or 128; head_dim 64 or 128 (bf16), 32, 64 or 128
- * (fp32); every array 16-byte aligned.  Pages may be shared by sequences that
+ * (fp32); k, v and pos 16-byte aligned, the other arrays of 4-byte numbers, here
+ * and in the calls below, 4-byte aligned.  Pages may be shared by sequences that
  * only read them: append, eviction and attention that accumulates weights write
  * the pages of their sequences, which then no other sequence of the call holds
  * (nor the same one twice).  Sequences of a call are rows 0 .. B-1 of the table,

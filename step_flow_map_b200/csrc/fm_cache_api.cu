@@ -22,6 +22,13 @@ constexpr int64_t MAX_ROWS = 1 << 24;      // new rows of a call, rows of a sequ
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
+// 4-byte numbers on the device: a misaligned address would be a fault there.
+template <typename... P>
+fm_status check_aligned4(const char* names, P... p) {
+  if ((((uintptr_t)p | ...) & 3) != 0) return set_err(FM_ERR_ARG, "%s must be 4-byte aligned", names);
+  return FM_OK;
+}
+
 fm_status check_cache(const fm_paged_cache* c) {
   if (!c || !c->k || !c->v || !c->page_table) return set_err(FM_ERR_ARG, "NULL argument");
   if (c->dtype != FM_F32 && c->dtype != FM_BF16)
@@ -127,6 +134,7 @@ extern "C" fm_status fm_cache_append(const fm_paged_cache* c, const fm_append_ar
   if (!a) return set_err(FM_ERR_ARG, "NULL argument");
   FM_TRY(check_rows(c, a->T, a->B, a->n_heads));
   if (!a->cu_rows || !a->kv_len) return set_err(FM_ERR_ARG, "NULL argument");
+  FM_TRY(check_aligned4("cu_rows, kv_len and q_pos", a->cu_rows, a->kv_len, a->q_pos));
   if (a->rot_dim < 0 || a->rot_dim > c->head_dim || a->rot_dim % 16)
     return set_err(FM_ERR_ARG, "rot_dim %d is not a multiple of 16 up to head_dim %d", a->rot_dim,
                    c->head_dim);
@@ -375,6 +383,7 @@ extern "C" fm_status fm_cache_attention(const fm_paged_cache* c, const fm_attent
                                         void* ws, size_t ws_bytes, fm_stream stream) {
   FM_TRY(check_attention(c, a));
   if (!a->cu_rows || !a->kv_len) return set_err(FM_ERR_ARG, "NULL argument");
+  FM_TRY(check_aligned4("cu_rows, kv_len, q_pos and lse", a->cu_rows, a->kv_len, a->q_pos, a->lse));
   if (!(a->scale > 0.f) || a->scale > 1e30f)
     return set_err(FM_ERR_ARG, "scale must be finite and > 0");
   if (c->pos && !a->q_pos) return set_err(FM_ERR_ARG, "a cache with positions needs q_pos");
@@ -433,6 +442,7 @@ extern "C" fm_status fm_cache_evict(const fm_paged_cache* c, const int32_t* kv_l
                                     int recent, int32_t* new_len, fm_stream stream) {
   FM_TRY(check_cache(c));
   if (!kv_len || !next_pos || !new_len) return set_err(FM_ERR_ARG, "NULL argument");
+  FM_TRY(check_aligned4("kv_len, next_pos and new_len", kv_len, next_pos, new_len));
   if (!c->pos || !c->weight) return set_err(FM_ERR_ARG, "eviction needs cache->pos and cache->weight");
   if (B < 1 || max_kv < 1 || budget < 1) return set_err(FM_ERR_ARG, "sizes must be positive");
   if (B > FM_MAX_CALL_SEQS)
