@@ -398,7 +398,8 @@ fm_status fm_cache_attention(const fm_paged_cache *cache, const fm_attention_arg
  * evicted rows' places below it, keys, values, positions and weights; the
  * other rows stay where they are.
  *   kv_len, next_pos  device [B]: cached rows; the next token's position
- *   new_len           device [B] out: min(kv_len, budget); not kv_len itself
+ *   new_len           device [B] out: min(kv_len, budget); overlaps neither of
+ *                     the two above
  * Needs cache->pos and cache->weight, pages that no other sequence of the
  * call holds, sinks + recent <= budget and max_kv (no sequence is longer)
  * <= FM_MAX_EVICT_ROWS (else FM_ERR_UNSUPPORTED).  Exact. */

@@ -452,7 +452,10 @@ extern "C" fm_status fm_cache_evict(const fm_paged_cache* c, const int32_t* kv_l
   if (sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
     return set_err(FM_ERR_ARG, "sinks %d and recent %d must not be negative nor exceed the budget %d",
                    sinks, recent, budget);
-  if (new_len == kv_len) return set_err(FM_ERR_ARG, "new_len must not be kv_len");
+  // a sequence's CTAs read its length and position while the first of them writes
+  for (const int32_t* in : {kv_len, next_pos})
+    if ((uintptr_t)new_len < (uintptr_t)(in + B) && (uintptr_t)in < (uintptr_t)(new_len + B))
+      return set_err(FM_ERR_ARG, "new_len must not overlap kv_len or next_pos");
   fm::EvictArgs k;
   k.c = view(c);
   k.kv_len = kv_len;

@@ -20,3 +20,11 @@ def test_misaligned_outputs_and_lengths_are_refused(off):
     for i in range(3):
         kv, nxt, new = (p + off * (i == j) for j, p in enumerate(at))
         refused(fmb.FM_ERR_ARG, fmb.fm_cache_evict, cache(), kv, nxt, 2, 64, 32, 4, 8, new)
+
+
+@pytest.mark.parametrize("d", [0, 4, 28, -4, -28])
+def test_eviction_refuses_lengths_that_overlap_its_inputs(d):
+    """Eight sequences: the new lengths lie d bytes from the old ones, or from the positions."""
+    kv, nxt = P, P + 4096
+    refused(fmb.FM_ERR_ARG, fmb.fm_cache_evict, cache(), kv, nxt, 8, 64, 32, 4, 8, kv + d)
+    refused(fmb.FM_ERR_ARG, fmb.fm_cache_evict, cache(), kv, nxt, 8, 64, 32, 4, 8, nxt + d)
