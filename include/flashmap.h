@@ -333,7 +333,7 @@ typedef struct {
  *                0: no rotation.  rot_dim: a multiple of 16, at most head_dim
  *   interleaved  0: pair i is values (i, i + rot_dim/2); 1: (2i, 2i + 1)
  *   q_out        device [T] rows of [n_heads, head_dim], q_out_stride apart;
- *                may be q itself (same stride)
+ *                may be q itself (same stride), else overlaps none of q, k, v
  * The rows' keys (after norm and rotation) and values go to their cache rows;
  * with cache->pos their positions, with cache->weight zeros.  Sums, norms and
  * angles are fp32 (angles reduced in fp64), each output rounded once. */
@@ -372,8 +372,8 @@ fm_status fm_cache_append(const fm_paged_cache *cache, const fm_append_args *a, 
  * to bf16.  Results do not depend on scheduling.
  * ws: device, 256-byte aligned, at least what fm_cache_attention_workspace
  * says for the same sizes on the current device; its contents need no set-up
- * and mean nothing afterwards.  out must not overlap q.  Calls that may overlap on the device (two
- * streams, two graphs) need a workspace each. */
+ * and mean nothing afterwards.  q, out and lse must not overlap.  Calls that
+ * may overlap on the device (two streams, two graphs) need a workspace each. */
 typedef struct {
   int T, B, n_heads, max_rows, max_kv;
   const void *q;

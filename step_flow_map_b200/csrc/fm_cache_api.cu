@@ -94,6 +94,37 @@ fm_status check_stride(const fm_paged_cache* c, const char* name, const void* p,
   return FM_OK;
 }
 
+// Rows of `width` bytes, `stride` bytes apart.
+struct RowSet {
+  uintptr_t at;
+  int64_t stride, width;
+  int64_t n;
+  uintptr_t end() const { return at + (uintptr_t)((n - 1) * stride + width); }
+};
+RowSet row_set(const fm_paged_cache* c, const void* p, int64_t stride, int heads, int T) {
+  return {(uintptr_t)p, stride * esize(c), (int64_t)heads * c->head_dim * esize(c), T};
+}
+int64_t floor_div(int64_t x, int64_t y) { return x / y - (x % y < 0); }
+// Whether two sets of as many rows share a byte.  Slices of one buffer lie row
+// by row between one another, so their extents may meet though they share
+// nothing.
+bool overlap(const RowSet& a, const RowSet& b) {
+  if (a.at >= b.end() || b.at >= a.end()) return false;
+  if (a.n == 1) return true;
+  if (a.stride == b.stride) {
+    // row i of a meets row i + k of b iff -b.width < d + k stride < a.width
+    const int64_t d = (int64_t)(b.at - a.at);
+    const int64_t lo = floor_div(-b.width - d, a.stride) + 1, hi = -floor_div(d - a.width, a.stride) - 1;
+    return std::max(lo, 1 - a.n) <= std::min(hi, a.n - 1);
+  }
+  for (int64_t i = 0, j = 0; i < a.n && j < b.n;) {   // in the order of the addresses
+    const uintptr_t x = a.at + (uintptr_t)(i * a.stride), y = b.at + (uintptr_t)(j * b.stride);
+    if (x < y + (uintptr_t)b.width && y < x + (uintptr_t)a.width) return true;
+    x < y ? ++i : ++j;
+  }
+  return false;
+}
+
 // SM count of the current device, asked once per device.
 fm_status device_sms(int* sms) {
   static std::mutex mu;
@@ -150,6 +181,14 @@ extern "C" fm_status fm_cache_append(const fm_paged_cache* c, const fm_append_ar
   FM_TRY(check_stride(c, "k", a->k, a->k_stride, c->n_kv_heads, a->T));
   FM_TRY(check_stride(c, "v", a->v, a->v_stride, c->n_kv_heads, a->T));
   FM_TRY(check_stride(c, "q_out", a->q_out, a->q_out_stride, a->n_heads, a->T));
+  // a row's values are loaded while the row before it is stored, keys and values
+  // by other threads than its queries: only a row in its own place is safe
+  const RowSet qo = row_set(c, a->q_out, a->q_out_stride, a->n_heads, a->T);
+  const bool in_place = a->q_out == a->q && (a->T == 1 || a->q_out_stride == a->q_stride);
+  if ((!in_place && overlap(qo, row_set(c, a->q, a->q_stride, a->n_heads, a->T))) ||
+      overlap(qo, row_set(c, a->k, a->k_stride, c->n_kv_heads, a->T)) ||
+      overlap(qo, row_set(c, a->v, a->v_stride, c->n_kv_heads, a->T)))
+    return set_err(FM_ERR_ARG, "q_out overlaps q, k or v (only q itself with its stride is allowed)");
   fm::AppendArgs k;
   k.c = view(c);
   k.T = a->T;
@@ -390,7 +429,11 @@ extern "C" fm_status fm_cache_attention(const fm_paged_cache* c, const fm_attent
   if (a->T == 0) return FM_OK;
   FM_TRY(check_stride(c, "q", a->q, a->q_stride, a->n_heads, a->T));
   FM_TRY(check_stride(c, "out", a->out, a->out_stride, a->n_heads, a->T));
-  if (a->out == a->q) return set_err(FM_ERR_ARG, "out must not be q");
+  const RowSet out = row_set(c, a->out, a->out_stride, a->n_heads, a->T);
+  const RowSet lse = {(uintptr_t)a->lse, a->n_heads * 4, a->n_heads * 4, a->T};
+  const RowSet q = row_set(c, a->q, a->q_stride, a->n_heads, a->T);
+  if (overlap(out, q) || (a->lse && (overlap(lse, out) || overlap(lse, q))))
+    return set_err(FM_ERR_ARG, "q, out and lse must not overlap");
   if (!ws || ((uintptr_t)ws & 255)) return set_err(FM_ERR_ARG, "workspace must be 256-byte aligned");
   AttnPlan p;
   FM_TRY(plan_attention(c, a, &p));

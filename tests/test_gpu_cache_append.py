@@ -72,3 +72,24 @@ def test_a_gain_scales_values_past_the_rotation_by_themselves(dtype, dh, inter):
     got[..., rot + 3] = want[..., rot + 3]
     tol = (U[dtype] + 2.0 ** -21) * np.abs(want) + 2.0 ** -20 * np.abs(want).max(-1, keepdims=True) * (np.arange(dh) < rot)
     assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 40, 3000])
+@pytest.mark.parametrize("where", ["in place", "beside"])
+def test_queries_go_to_a_slice_of_the_same_buffer(dtype, T, where):
+    """The projection's own query slice, or another slice of the same rows."""
+    hq, hkv, dh = 8, 2, 64
+    w = World([T + 5], hkv, dh, 16, dtype, seed=T)
+    wide = torch.tensor(w.rng.normal(size=(T, 2 * hq + 2 * hkv, dh))).to(DT[dtype]).cuda()
+    q, k, v, spare = wide.split([hq, hkv, hkv, hq], 1)
+    f = torch.tensor([0.5 ** i for i in range(16)], dtype=torch.float64).cuda()
+    gain = torch.tensor(w.rng.normal(size=dh)).to(DT[dtype]).cuda()
+    args = dict(cu_rows=cu_of([T]), kv_len=w.kv, q_gain=gain, k_gain=gain, inv_freq=f)
+    want = w.cache.append(q, k, v, **args)
+    cached = w.k.clone(), w.v.clone()
+    out = q if where == "in place" else spare
+    got = w.cache.append(q, k, v, **args, out=out)
+    assert got.data_ptr() == out.data_ptr() and torch.equal(got, want)
+    for now, old in zip((w.k, w.v), cached):
+        assert torch.equal(torch.nan_to_num(now, 9.0), torch.nan_to_num(old, 9.0))
