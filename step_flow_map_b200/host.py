@@ -188,6 +188,13 @@ class PagedCache:
             self._check("q_pos", q_pos, torch.int32, (T,))
         return B
 
+    @staticmethod
+    def _sizes(**given):
+        """Whole numbers that the C structures hold in 32 bits (ctypes would wrap larger ones)."""
+        for name, x in given.items():
+            if not -2**31 <= x < 2**31:
+                raise ValueError(f"{name} = {x} does not fit 32 bits")
+
     def _on(self, stream, *lent):
         """A context under which tensors are allocated on the cache's device and on
         `stream` (None: the device's current stream), and that stream, to which the
@@ -247,6 +254,7 @@ class PagedCache:
         T, n_heads, dh = q.shape
         qs = self._rows("q", q, T, n_heads)
         B = self._seqs(T, cu_rows, kv_len, q_pos)
+        self._sizes(max_rows=max_rows, max_kv=max_kv, window=window, sinks=sinks)
         ctx, st = self._on(stream, q, cu_rows, kv_len, q_pos, out)
         with ctx:
             if out is None:
@@ -277,6 +285,7 @@ class PagedCache:
         self._check("next_pos", next_pos, torch.int32, (B,))
         if B > self._table.shape[0]:
             raise ValueError(f"{B} sequences, {self._table.shape[0]} rows of page_table")
+        self._sizes(max_kv=max_kv, budget=budget, sinks=sinks, recent=recent)
         ctx, st = self._on(stream, kv_len, next_pos, new_len)
         with ctx:
             if new_len is None:

@@ -1,8 +1,10 @@
 """Calls of the paged cache that would fault, race or mean something else on the GPU are
 refused on the host (no GPU needed)."""
 import pytest
+import torch
 
 import step_flow_map_b200 as fmb
+from step_flow_map_b200.host import PagedCache
 from test_cache_host import P, _lib, append_args, attn_args, cache, refused  # noqa: F401
 
 
@@ -105,3 +107,28 @@ def test_bad_append_is_refused_for_its_own_reason(kw, status):
     with pytest.raises(fmb.FlashmapError) as e:
         fmb.fm_cache_append(cache(), append_args(**{**AT, **kw}))
     assert e.value.status == status and "overlap" not in str(e.value)
+
+
+# ------------------------------------------------------------------ numbers that C would wrap
+@pytest.mark.parametrize("name", ["max_rows", "max_kv", "window", "sinks"])
+@pytest.mark.parametrize("x", [2 ** 31, 2 ** 32, 2 ** 32 + 7, 2 ** 64 + 5, -2 ** 31 - 1])
+def test_attend_refuses_numbers_past_32_bits(name, x):
+    c, q, cu, kv, _ = a_cache_off_the_gpu()
+    with pytest.raises(ValueError, match=name):
+        c.attend(q, cu, kv, **{**dict(max_rows=4, max_kv=16, window=3, sinks=1), name: x})
+
+
+@pytest.mark.parametrize("name", ["max_kv", "budget", "sinks", "recent"])
+@pytest.mark.parametrize("x", [2 ** 31, 2 ** 32, 2 ** 32 + 7, 2 ** 64 + 5, -2 ** 31 - 1])
+def test_evict_refuses_numbers_past_32_bits(name, x):
+    c, _, _, kv, _ = a_cache_off_the_gpu()
+    with pytest.raises(ValueError, match=name):
+        c.evict(kv, kv, **{**dict(budget=8, max_kv=16, sinks=1, recent=2), name: x})
+
+
+def a_cache_off_the_gpu():
+    """Calls with it end in ValueError at the latest when they ask for its GPU."""
+    k = torch.zeros(6, 2, 16, 64, dtype=torch.bfloat16)
+    c = PagedCache(k, k.clone(), torch.zeros(2, 3, dtype=torch.int32), None, torch.zeros(6, 2, 16))
+    return (c, torch.zeros(4, 4, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32),
+            torch.zeros(2, dtype=torch.int32), torch.zeros(4, 2, 64, dtype=torch.bfloat16))
