@@ -5,10 +5,12 @@ The library lands next to this file, so it travels with the source tree.
 """
 from __future__ import annotations
 
+import hashlib
 import os
 import re
 import subprocess
 import sys
+import time
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -41,22 +43,38 @@ def link_command(objs, out: str = LIB) -> list:
 def sources() -> list:
     csrc = os.path.join(HERE, "csrc")
     files = [os.path.join(csrc, f) for f in os.listdir(csrc)]
-    files.append(os.path.join(ROOT, "include", "flashmap.h"))
+    files += [os.path.join(ROOT, "include", "flashmap.h"), os.path.join(HERE, "build.py")]
     return files
 
 
-def up_to_date() -> bool:
+def object_file(src: str, extra=()) -> str:
+    """Where a source's object is kept: one file for every way to compile it."""
+    cmd = "\n".join(compile_command(src, "", extra)).replace(ROOT, "")
+    return os.path.join(OBJ_DIR, f"{os.path.basename(src)}.{hashlib.sha1(cmd.encode()).hexdigest()[:12]}.o")
+
+
+def _linked() -> str:
+    return os.path.join(OBJ_DIR, os.path.basename(LIB) + ".linked")
+
+
+def up_to_date(extra=()) -> bool:
+    """Whether the library is newer than its sources and, where it is known what it
+    was linked from, was compiled with these flags."""
     if not os.path.exists(LIB):
         return False
+    if os.path.exists(_linked()):
+        with open(_linked(), encoding="utf-8") as f:
+            if f.read().split() != [os.path.basename(object_file(s, extra)) for s in SRCS]:
+                return False
     t = os.path.getmtime(LIB)
     return all(os.path.getmtime(f) <= t for f in sources())
 
 
 def _newest(src: str, seen=None) -> float:
-    """Latest change of a source and of the headers it includes."""
+    """Latest change of a source, of the headers it includes and of this file."""
     seen = set() if seen is None else seen
     seen.add(src)
-    t = os.path.getmtime(src)
+    t = max(os.path.getmtime(src), os.path.getmtime(os.path.join(HERE, "build.py")))
     for name in re.findall(r'#include "([^"]+)"', open(src, encoding="utf-8").read()):
         for d in (os.path.dirname(src), os.path.join(ROOT, "include")):
             f = os.path.join(d, name)
@@ -82,21 +100,36 @@ def _run(cmds, verbose: bool) -> None:
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Compile every source (side by side) and link the library.  Objects
-    newer than their source and its headers are kept unless `force`."""
-    if not force and up_to_date():
+    newer than their source and its headers, and compiled with the same flags,
+    are kept unless `force`.  Every file appears under its name when it is whole, so
+    processes that build at once do no harm."""
+    if not force and up_to_date(extra):
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
-    objs, cmds = [], []
-    for src in SRCS:
-        obj = os.path.join(OBJ_DIR, os.path.basename(src) + ".o")
-        objs.append(obj)
-        if force or not os.path.exists(obj) or os.path.getmtime(obj) < _newest(src):
-            cmds.append(compile_command(src, obj, extra))
-    _run(cmds, verbose)
-    tmp = LIB + ".tmp"
-    _run([link_command(objs, tmp)], verbose)
-    os.replace(tmp, LIB)
+    start = time.time()            # a source that changes from here on is newer than what is made of it
+    tmp = f".{os.getpid()}.tmp"
+    objs = [object_file(src, extra) for src in SRCS]
+    stale = [(src, obj) for src, obj in zip(SRCS, objs)
+             if force or not os.path.exists(obj) or os.path.getmtime(obj) < _newest(src)]
+    try:
+        _run([compile_command(src, obj + tmp, extra) for src, obj in stale], verbose)
+        for _, obj in stale:
+            _appear(obj, tmp, start)
+        _run([link_command(objs, LIB + tmp)], verbose)
+        with open(_linked() + tmp, "w", encoding="utf-8") as f:
+            f.write(" ".join(map(os.path.basename, objs)))
+        _appear(LIB, tmp, start)
+        _appear(_linked(), tmp, start)
+    finally:
+        for f in [*objs, LIB, _linked()]:
+            if os.path.exists(f + tmp):
+                os.remove(f + tmp)
     return LIB
+
+
+def _appear(path: str, tmp: str, when: float) -> None:
+    os.utime(path + tmp, (when, when))
+    os.replace(path + tmp, path)
 
 
 if __name__ == "__main__":
