@@ -189,28 +189,50 @@ def _strip_comments(text: str) -> str:
     return "\n".join(ln for ln in lines if ln)
 
 
-def source_sha1(root: str = ROOT) -> str:
+def _included(path: str, seen: dict) -> dict:
+    """{file: text without comments} of a source and of the files beside it that it includes."""
+    import re
+    if path not in seen and os.path.exists(path):
+        with open(path, encoding="utf-8") as fh:
+            seen[path] = _strip_comments(fh.read())
+        for name in re.findall(r'#include "([^"]+)"', seen[path]):
+            _included(os.path.join(os.path.dirname(path), name), seen)
+    return seen
+
+
+def source_sha1(root: str = ROOT, kernel: str | None = None) -> str:
     """Hash of the kernel sources without comments; a stored ncu traffic
     figure is reported only while it matches (the kernels have not changed
-    since the capture)."""
+    since the capture).  With `kernel`: of the files that it is made from and launched by,
+    that is the one that defines it, those which that one includes, and the
+    translation units that reach it; of all sources where no file defines it."""
     import hashlib
-    h = hashlib.sha1()
+    import re
     csrc = os.path.join(root, "step_flow_map_b200", "csrc")
-    for f in sorted(os.listdir(csrc)) + ["../../include/flashmap.h"]:
+    names = sorted(os.listdir(csrc)) + ["../../include/flashmap.h"]
+    if kernel:
+        made = {f: _included(os.path.join(csrc, f), {}) for f in names}
+        defines = re.compile(r"__global__[^;{]*\b" + re.escape(kernel) + r"\s*\(")
+        home = [f for f in names if defines.search(made[f][os.path.join(csrc, f)])]
+        if home:
+            names = [f for f in names if any(
+                os.path.join(csrc, f) in made[h] or f.endswith(".cu") and os.path.join(csrc, h) in made[f] for h in home)]
+    h = hashlib.sha1()
+    for f in names:
         with open(os.path.join(csrc, f), encoding="utf-8") as fh:
             h.update(f.encode() + _strip_comments(fh.read()).encode())
     return h.hexdigest()
 
 
-def stored_traffic(kernel: str, workload: str, path: str | None = None):
+def stored_traffic(kernel: str, workload: str, path: str | None = None, root: str = ROOT):
     """DRAM bytes per launch from profiles/traffic.txt (JSON), or None."""
-    p = path or os.path.join(ROOT, "profiles", "traffic.txt")
+    p = path or os.path.join(root, "profiles", "traffic.txt")
     if not os.path.exists(p):
         return None
     with open(p) as f:
         d = json.load(f)
     e = d.get(kernel, {}).get(workload)
-    if e and e.get("source_sha1") == source_sha1():
+    if e and e.get("source_sha1") == source_sha1(root, kernel):
         return e["dram_bytes_per_launch"]
     return None
 
