@@ -371,6 +371,9 @@ fm_status fm_cache_append(const fm_paged_cache *cache, const fm_append_args *a, 
  * and outputs are fp32; bf16 probabilities enter the value product rounded
  * to bf16.  Results do not depend on scheduling.
  * ws: device, 256-byte aligned, at least what fm_cache_attention_workspace
+ * (some MB; with accumulate and at most 16 new rows x query heads per key/value
+ * head 4 bytes more for each of these and each cached row of a head: of B max_kv
+ * rows or of all that the cache holds, whichever is less)
  * says for the same sizes on the current device; its contents need no set-up
  * and mean nothing afterwards.  q, out and lse must not overlap.  Calls that
  * may overlap on the device (two streams, two graphs) need a workspace each. */

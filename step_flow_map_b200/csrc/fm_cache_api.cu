@@ -232,7 +232,7 @@ struct AttnPlan {
   enum { DECODE, TC_ONE, TC_PAIR, SIMT } kind = SIMT;
   int qt = 0, rt = 0, tile_rows = 0, ov = 0, grid = 0;   // rows of a partial; see CacheAttnArgs
   int64_t tiles = 0;
-  bool keep = false;
+  int score_units = 0;
   size_t o_first = 0, o_tile = 0, o_join = 0, o_lse = 0, o_scores = 0, o_ml = 0, o_part = 0, total = 0;
 };
 
@@ -286,11 +286,20 @@ fm_status plan_attention(const fm_paged_cache* c, const fm_attention_args* a, At
   at = up256(at + (size_t)p->grid * 2 * sizeof(int4));
   p->o_lse = at;
   if (a->accumulate) at = up256(at + (size_t)a->T * a->n_heads * sizeof(float));
-  // scores of few packed rows are kept for the weights (see score_at)
-  p->keep = a->accumulate && rows <= 16;
+  // scores of few packed rows are kept for the weights, unit by unit (see
+  // score_at): no more units than max_kv allows, or than the cache has rows for
+  // (no page is in two tables of a call that writes weights), so they take 1/32
+  // of the keys' and values' bytes at four packed rows of width 128 in bf16, 1/8
+  // at sixteen.  (64 sequences of which one has 65,536 rows, the others 2,048: 24 MB
+  // against 512 MB by max_kv alone, in the same time.)
   p->o_scores = at;
-  if (p->keep)
-    at = up256(at + (size_t)a->B * c->n_kv_heads * ((a->max_kv + 15) / 16) * rows * 64);
+  if (a->accumulate && rows <= 16) {
+    const int64_t bytes = fm::CD_KB * rows * (int64_t)sizeof(float);
+    const int64_t blocks = std::min((int64_t)a->B * ((a->max_kv + fm::CD_KB - 1) / fm::CD_KB),
+                                    (int64_t)c->n_pages * c->page_size / fm::CD_KB + a->B);
+    p->score_units = (int)(blocks * c->n_kv_heads);
+    at = up256(at + (size_t)(p->score_units * bytes));
+  }
   p->o_ml = at;
   at = up256(at + (size_t)p->grid * 2 * p->qt * sizeof(float2));
   p->o_part = at;
@@ -391,8 +400,8 @@ fm_status run_attention(const fm::CacheAttnArgs& k, const AttnPlan& p, int accum
   auto grid = [&](int per) {
     return dim3((unsigned)std::max(1, std::min((k.max_kv + per - 1) / per, 256)), k.c.n_kv, k.B);
   };
-  if (k.scores) {
-    FM_LAUNCH_OK("cache weights", fm::launch_pdl(fm::k_cache_weights_scores, grid(fm::CW_THREADS),
+  if (p.kind == AttnPlan::DECODE) {
+    FM_LAUNCH_OK("cache weights", fm::launch_pdl(fm::k_cache_weights_scores<T, DH>, grid(fm::CW_THREADS),
                                                  dim3(fm::CW_THREADS), 0, st, k));
   } else if constexpr (std::is_same<T, bf16>::value) {
     auto kernel = fm::k_cache_weights_mma<DH>;
@@ -469,7 +478,8 @@ extern "C" fm_status fm_cache_attention(const fm_paged_cache* c, const fm_attent
   k.plan_join = (int4*)(w + p.o_join);
   k.part_ml = (float2*)(w + p.o_ml);
   k.part = (float*)(w + p.o_part);
-  k.scores = p.keep ? (float*)(w + p.o_scores) : nullptr;
+  k.scores = (float*)(w + p.o_scores);
+  k.score_units = p.score_units;
   cudaStream_t st = (cudaStream_t)stream;
   if (c->dtype == FM_BF16)
     return c->head_dim == 128 ? run_attention<bf16, 128>(k, p, a->accumulate, st)

@@ -12,7 +12,7 @@
 // equal runs, whatever the lengths.  A CTA keeps (max, sum, O) over the
 // blocks of a tile that fall in its run and writes the result when it had all
 // of them, else a partial; at most two partials per CTA (its first and its
-// last tile), so the workspace does not grow with the lengths.  A second
+// last tile), so their number does not grow with the lengths.  A second
 // kernel joins the partials of split tiles in CTA order.
 #pragma once
 #include "fm_cache.cuh"
@@ -35,13 +35,15 @@ struct CacheAttnArgs {
   float* lse;                      // or null
   // workspace
   int* plan_n;                     // number of tiles
-  int* plan_first;                 // [tiles + 1]: first unit of each tile, heads apart
+  int* plan_first;                 // [tiles + 1]: first unit of each tile, heads apart; few packed
+                                   //   rows: [B + 1], of each sequence
   int4* plan_tile;                 // [tiles][2]: (b, first packed row, first new row, packed rows
                                    //   of the sequence), (s_end, lo, hi, position of new row 0)
   int4* plan_join;                 // [grid][2], see JoinItem
   float* part;                     // [grid][2][QT][DH]
   float2* part_ml;                 // [grid][2][QT]: (max, sum), log2 units
-  float* scores;                   // see score_at, or null
+  float* scores;                   // see score_at
+  int score_units;                 // units it has room for
 };
 
 // Rows a tile can see: [0, s_end) and [lo, hi), s_end <= lo.
@@ -75,6 +77,10 @@ struct SeenBlocks {
     nb = max(1, ns + max(0, (r.hi + KB - 1) / KB - b0));
   }
   __device__ __forceinline__ int row(int j) const { return (j < ns ? j : j - ns + b0) * KB; }
+  __device__ __forceinline__ int at(int r) const {   // the block of a row that is seen
+    const int j = r / KB;
+    return j < ns ? j : j - b0 + ns;
+  }
 };
 __device__ __forceinline__ bool row_seen(const SeenRows& s, int r) {
   return r < s.s_end || (r >= s.lo && r < s.hi);
@@ -85,11 +91,12 @@ __device__ __forceinline__ bool sees(int pq, int pk, int window, int sinks) {
   return pk <= pq && (window == 0 || (unsigned)pq - (unsigned)pk < (unsigned)window || pk < sinks);
 }
 
-// Masked scores (log2 units) of the cache row r of (b, g) against packed row x
-// of at most a.max_rows G <= 16, 16 neighbouring cache rows side by side.
-__device__ __forceinline__ size_t score_at(const CacheAttnArgs& a, int b, int g, int r, int x) {
-  const size_t tiles = (size_t)((a.max_kv + 15) >> 4);
-  return ((((size_t)b * a.c.n_kv + g) * tiles + (r >> 4)) * (a.max_rows * a.G) + x) * 16 + (r & 15);
+constexpr int CD_KB = 64;          // cache rows of a unit of few packed rows
+// Masked scores (log2 units) of the 16 cache rows `sub` of unit u (CD_KB rows of a
+// sequence and head, numbered over the call) against packed row x of at most
+// a.max_rows G <= 16, the 16 rows' side by side.
+__device__ __forceinline__ size_t score_at(const CacheAttnArgs& a, int u, int sub, int x) {
+  return (((size_t)u * 4 + sub) * (a.max_rows * a.G) + x) * 16;
 }
 
 // ------------------------------------------------------------------ plan
@@ -534,14 +541,43 @@ __global__ void __launch_bounds__(CJ_THREADS) k_cache_join_cols(const CacheAttnA
 // weight_r += sum over queries and heads of e^(s - lse), added up in the order
 // of the packed rows (no atomics, so the sum does not depend on scheduling).
 
+constexpr int CW_THREADS = 256;
+
+// One cached row by the whole warp, the key in registers, the scores once more.
+template <typename T, int DH>
+__device__ __forceinline__ void weigh_row(const CacheAttnArgs& a, const NewRows& s, int n, int g, int r,
+                                          size_t at) {
+  const int lane = threadIdx.x & 31;
+  const int pk = a.c.pos ? a.c.pos[at] : r;
+  float kv[DH / 32];
+#pragma unroll
+  for (int k = 0; k < DH / 32; ++k) kv[k] = to_f(((const T*)a.c.k)[at * DH + lane + 32 * k]);
+  float sum = 0.f;
+  for (int x = 0; x < n * a.G; ++x) {
+    const int t = s.first + x / a.G, h = g * a.G + x % a.G;
+    const int pq = a.q_pos ? __ldg(a.q_pos + t) : s.L - s.n + x / a.G;
+    if (!sees(pq, pk, a.window, a.sinks)) continue;
+    float d = 0.f;
+#pragma unroll
+    for (int k = 0; k < DH / 32; ++k)
+      d = fmaf(to_f(((const T*)a.q)[t * a.qs + h * DH + lane + 32 * k]), kv[k], d);
+    d = warp_sum(d);
+    sum += exp2f(d * a.scale_log2 - a.lse[(size_t)t * a.n_heads + h] * 1.4426950408889634f);
+  }
+  if (lane == 0) a.c.weight[at] += sum;
+}
+
 // Few packed rows: from the scores the attention kernel left, a thread per
 // cache row.  Bound: HBM, 4 bytes per score and 8 per weight -- for four query
 // heads per key/value head 24 bytes a row against the 256 that reading the
-// keys again would take.
-constexpr int CW_THREADS = 256;
+// keys again would take.  Units that the scores have no room for (lengths past
+// the rows that the cache has: pages that do not exist) go row by row; to do
+// so for all rows would take 1,195 us where the scores take 216 (64 sequences of
+// 4,096 rows, 8 heads, with the attention's 189).
+template <typename T, int DH>
 __global__ void __launch_bounds__(CW_THREADS) k_cache_weights_scores(const CacheAttnArgs a) {
   __shared__ float s_lse[16];
-  const int g = blockIdx.y, b = blockIdx.z;
+  const int g = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
   const NewRows s = new_rows(a.cu, a.kv_len, b, a.T);
@@ -554,24 +590,33 @@ __global__ void __launch_bounds__(CW_THREADS) k_cache_weights_scores(const Cache
   }
   __syncthreads();
   const SeenRows seen = seen_rows(a, s, 0, n - 1);
-  for (int r = blockIdx.x * CW_THREADS + threadIdx.x; r < seen.hi; r += gridDim.x * CW_THREADS) {
-    const int page = row_seen(seen, r) ? cache_page(a.c, b, r) : -1;
-    if (page < 0) continue;
-    float* w = a.c.weight + cache_row(a.c, page, g, r);
-    const float had = *w;
-    const float* p = a.scores + score_at(a, b, g, r, 0);
-    float sum = 0.f;
+  const SeenBlocks<CD_KB> blocks(seen);
+  const int first = a.plan_first[b];
+  const int u0 = first * a.c.n_kv + g * (a.plan_first[b + 1] - first);   // this head's first unit
+  for (int r0 = blockIdx.x * CW_THREADS + threadIdx.x - lane; r0 < seen.hi; r0 += gridDim.x * CW_THREADS) {
+    const int r = r0 + lane, u = u0 + blocks.at(r);
+    const int page = r < seen.hi && row_seen(seen, r) ? cache_page(a.c, b, r) : -1;
+    const size_t at = cache_row(a.c, max(page, 0), g, r);
+    if (page >= 0 && u < a.score_units) {
+      float* w = a.c.weight + at;
+      const float had = *w;
+      const float* p = a.scores + score_at(a, u, (r >> 4) & 3, 0) + (r & 15);
+      float sum = 0.f;
 #pragma unroll 4
-    for (int x = 0; x < rows; ++x) sum += exp2f(p[x * 16] - s_lse[x]);
-    *w = had + sum;
+      for (int x = 0; x < rows; ++x) sum += exp2f(p[x * 16] - s_lse[x]);
+      *w = had + sum;
+    }
+    for (unsigned rest = __ballot_sync(0xffffffffu, page >= 0 && u >= a.score_units); rest; rest &= rest - 1) {
+      const int i = __ffs((int)rest) - 1;
+      weigh_row<T, DH>(a, s, n, g, r0 + i, __shfl_sync(0xffffffffu, at, i));
+    }
   }
 }
 
-// Many packed rows, fp32: one warp per cache row, the key in registers, the
-// scores once more.
+// Many packed rows, fp32: one warp per cache row.
 template <typename T, int DH>
 __global__ void __launch_bounds__(CW_THREADS) k_cache_weights(const CacheAttnArgs a) {
-  const int lane = threadIdx.x & 31, g = blockIdx.y, b = blockIdx.z;
+  const int g = blockIdx.y, b = blockIdx.z;
   pdl_wait();
   pdl_trigger();
   const NewRows s = new_rows(a.cu, a.kv_len, b, a.T);
@@ -581,25 +626,7 @@ __global__ void __launch_bounds__(CW_THREADS) k_cache_weights(const CacheAttnArg
   for (int r = blockIdx.x * (CW_THREADS / 32) + (threadIdx.x >> 5); r < seen.hi;
        r += gridDim.x * (CW_THREADS / 32)) {
     const int page = row_seen(seen, r) ? cache_page(a.c, b, r) : -1;
-    if (page < 0) continue;
-    const size_t at = cache_row(a.c, page, g, r);
-    const int pk = a.c.pos ? a.c.pos[at] : r;
-    float kv[DH / 32];
-#pragma unroll
-    for (int k = 0; k < DH / 32; ++k) kv[k] = to_f(((const T*)a.c.k)[at * DH + lane + 32 * k]);
-    float sum = 0.f;
-    for (int x = 0; x < n * a.G; ++x) {
-      const int t = s.first + x / a.G, h = g * a.G + x % a.G;
-      const int pq = a.q_pos ? __ldg(a.q_pos + t) : s.L - s.n + x / a.G;
-      if (!sees(pq, pk, a.window, a.sinks)) continue;
-      float d = 0.f;
-#pragma unroll
-      for (int k = 0; k < DH / 32; ++k)
-        d = fmaf(to_f(((const T*)a.q)[t * a.qs + h * DH + lane + 32 * k]), kv[k], d);
-      d = warp_sum(d);
-      sum += exp2f(d * a.scale_log2 - a.lse[(size_t)t * a.n_heads + h] * 1.4426950408889634f);
-    }
-    if (lane == 0) a.c.weight[at] += sum;
+    if (page >= 0) weigh_row<T, DH>(a, s, n, g, r, cache_row(a.c, page, g, r));
   }
 }
 

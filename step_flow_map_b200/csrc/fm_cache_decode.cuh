@@ -23,7 +23,6 @@
 namespace fm {
 
 constexpr int CD_THREADS = 128;
-constexpr int CD_KB = 64;          // cache rows per unit
 constexpr int CD_STAGES = 3;
 constexpr int CD_QT = 16;
 
@@ -415,6 +414,8 @@ __global__ void __launch_bounds__(CD_THREADS, (CdCfg<T, DH>::CTAS)) k_cache_deco
   pdl_wait();
   pdl_trigger();
   decode_scan<CD_KB>(a, s, s_scan);
+  if (blockIdx.x == 0 && a.score_units > 0)            // for the weights
+    for (int b = tid; b <= a.B; b += CD_THREADS) a.plan_first[b] = s.first[b];
   const WorkRun w(s.first[256] * a.c.n_kv, gridDim.x);
   if ((int)blockIdx.x >= w.g || w.N == 0) {
     if (tid == 0) a.plan_join[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(CD_THREADS, (CdCfg<T, DH>::CTAS)) k_cache_deco
       if (here && (r0 < seen.s_end || (r0 + 16 > seen.lo && r0 < seen.hi))) {
         const DecodeKeys keys = {
             kt, kt + C::TILE, (const int*)(smb + warp * C::RING + stage * C::STAGE + 2 * C::TILE), r0,
-            a.scores ? a.scores + score_at(a, b, g, r0, 0) : nullptr,
+            u0 + done + it < a.score_units ? a.scores + score_at(a, u0 + done + it, warp, 0) : nullptr,
             !a.c.pos && r0 >= seen.lo && r0 + 15 <= p0 && r0 + 16 <= seen.hi &&
                 (a.window == 0 || tile.p_last - r0 < a.window)};
         state.tile(a, tile, keys, sq, merge + warp * C::SLOT);
