@@ -301,9 +301,11 @@ fm_status fm_verify_greedy_noalloc(const float *target_logits, const int32_t *dr
  * page_size is 16, 32, 64 or 128; head_dim 64 or 128 (bf16), 32, 64 or 128
  * (fp32); k, v and pos 16-byte aligned, the other arrays of 4-byte numbers, here
  * and in the calls below, 4-byte aligned.  Pages may be shared by sequences that
- * only read them: append, eviction and attention that accumulates weights write
- * the pages of their sequences, which then no other sequence of the call holds
- * (nor the same one twice).  Sequences of a call are rows 0 .. B-1 of the table,
+ * only read them: attention that accumulates weights and eviction write the
+ * pages of their sequences, append those that its new rows lie in, and a page that
+ * a call writes is held by no other sequence of the call (nor by the same one
+ * twice).  So drafts of one prefix may share its pages in append and in
+ * attention without weights.  Sequences of a call are rows 0 .. B-1 of the table,
  * B <= FM_MAX_CALL_SEQS. */
 typedef struct {
   int dtype, n_pages, page_size, n_kv_heads, head_dim, table_stride;
@@ -361,7 +363,10 @@ fm_status fm_cache_append(const fm_paged_cache *cache, const fm_append_args *a, 
  *   max_kv       no sequence is longer (a longer one is cut to it)
  *   scale        of the scores, > 0 (1/sqrt(head_dim) as a rule)
  *   accumulate   != 0: cache->weight[row] += the probabilities the row gets,
- *                summed over the new rows and the query heads of its head
+ *                summed over the new rows and the query heads of its head: all
+ *                of the call's new rows, drafted ones that a verifier rejects
+ *                afterwards among them (to count accepted rows only, attend
+ *                without it before the verify and score them once more after)
  *   lse          device [T, n_heads] fp32 log-sum-exp of the scores, or NULL
  * With cache->pos q_pos must be given; without it a new row's position is its
  * cache row, whatever q_pos says.  A query that sees nothing gets zeros and
@@ -400,8 +405,12 @@ fm_status fm_cache_attention(const fm_paged_cache *cache, const fm_attention_arg
  * The kept rows from cache row budget on move, in ascending order, into the
  * evicted rows' places below it, keys, values, positions and weights; the
  * other rows stay where they are.
- *   kv_len, next_pos  device [B]: cached rows; the next token's position
- *   new_len           device [B] out: min(kv_len, budget); overlaps neither of
+ * A row that does not exist ranks behind all others; what moves into its place
+ * is lost.  The attention after an eviction is that of the kept rows alone, so a
+ * target whose cache is cut has another distribution than one that keeps it all.
+ *   kv_len, next_pos  device [B]: cached rows (more than max_kv: cut to it first,
+ *                     whatever the rows past it weigh); the next token's position
+ *   new_len           device [B] out: min(kv_len, max_kv, budget); overlaps neither of
  *                     the two above
  * Needs cache->pos and cache->weight, pages that no other sequence of the
  * call holds, sinks + recent <= budget and max_kv (no sequence is longer)

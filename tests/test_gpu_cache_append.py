@@ -1,4 +1,4 @@
-"""What the paged cache's append passes on as it is.
+"""What the paged cache's append passes on as it is, and which pages it may share.
 
 Columns past rot_dim are not turned, and without a gain heads are not scaled: such
 values are copies, infinities and -0 among them, and are compared bit for bit (a
@@ -93,3 +93,29 @@ def test_queries_go_to_a_slice_of_the_same_buffer(dtype, T, where):
     assert got.data_ptr() == out.data_ptr() and torch.equal(got, want)
     for now, old in zip((w.k, w.v), cached):
         assert torch.equal(torch.nan_to_num(now, 9.0), torch.nan_to_num(old, 9.0))
+
+
+def test_sequences_may_share_the_pages_before_their_new_rows():
+    """Drafts of one prefix: each has its own last page, the pages before it are the same."""
+    w = World([64], 2, 64, 16, "bf16", extra=16, spare=6)
+    B, rows = 3, 5
+    own = [i for i in range(w.k.shape[0]) if i not in w.table[0, :4].tolist()][:B]
+    t = torch.tensor([w.table[0, :4].tolist() + [p] for p in own], dtype=torch.int32).cuda()
+    c = w.cache
+    c.page_table = t
+    old = w.k.clone(), w.v.clone()
+    kv = torch.full((B,), 64 + rows, dtype=torch.int32).cuda()
+    qkv = torch.tensor(w.rng.normal(size=(B * rows, 8, 64))).to(torch.bfloat16).cuda()
+    q = c.append(qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], cu_of([rows] * B), kv)
+    for i, (now, x) in enumerate(((w.k, qkv[:, 4:6]), (w.v, qkv[:, 6:]))):
+        want = old[i].clone()
+        for b, p in enumerate(own):
+            want[p, :, :rows] = x[b * rows:(b + 1) * rows].transpose(0, 1)
+        assert torch.equal(torch.nan_to_num(now, 9.0), torch.nan_to_num(want, 9.0))
+    out = c.attend(q, cu_of([rows] * B), kv, max_rows=rows, max_kv=64 + rows)
+    for b in range(B):
+        k, v = (torch.cat([x[p] for p in t[b].tolist()], 1)[:, :64 + rows].transpose(0, 1).double().cpu().numpy() for x in (w.k, w.v))
+        o, _, _, mag, _ = oc.attention(q[b * rows:(b + 1) * rows].double().cpu().numpy(), k, v, np.arange(64, 64 + rows),
+                                       np.arange(64 + rows)[:, None].repeat(2, 1), 64 ** -0.5)
+        # the bound of the attention tests with every score error below 2^-10
+        assert (np.abs(out[b * rows:(b + 1) * rows].double().cpu().numpy() - o) <= 2.0 ** -8 * np.abs(o) + 2.0 ** -6 * mag).all()

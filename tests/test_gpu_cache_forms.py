@@ -5,7 +5,7 @@ import torch
 
 import step_flow_map_b200 as fmb
 from oracle import cache as oc
-from test_gpu_cache import World, check_attention
+from test_gpu_cache import World, check_attention, cu_of
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,36 @@ def test_weights_of_lengths_past_the_rows_that_the_cache_has(dtype, rows, G, win
             want[w.table[b, r // 16], :, r % 16] += wt[r]
     # p off by 4 d = 2^-21 (dh + 8) big + 2^-18 relatively, with sum |q k| scale below 32: 2^-9.8; the weight is rounded once
     assert (np.abs(got - want) <= 2.0 ** -9.8 * (want + 1e-7) + 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [2, 8])
+def test_weights_of_accepted_rows_alone(dtype, G):
+    """A scored block whose drafts are accepted in part: attended without weights, and the rows that
+    stay once more with them.  The rejected rows leave no weight behind, and the next block takes
+    their places."""
+    rows, lens, accepted = 17, [150, 90, 133], [5, 17, 1]
+    w = World(lens, 2, 64, 16, dtype, seed=G, weight=True)
+    q = torch.tensor(w.rng.normal(size=(3 * rows, 2 * G, 64))).to(w.k.dtype).cuda()
+    cu = cu_of([rows] * 3)
+    before = [w.get(w.weight, b) for b in range(3)]
+    full = w.cache.attend(q, cu, w.kv, max_rows=rows, max_kv=150)
+    for b in range(3):
+        assert np.array_equal(w.get(w.weight, b), before[b])
+    kept = torch.cat([q[b * rows:b * rows + n] for b, n in enumerate(accepted)])
+    short = [L - rows + n for L, n in zip(lens, accepted)]
+    again = w.cache.attend(kept, cu_of(accepted), torch.tensor(short, dtype=torch.int32).cuda(), max_rows=rows, max_kv=150,
+                           accumulate=True)
+    at = 0
+    for b, (L, n) in enumerate(zip(short, accepted)):
+        k, v = (w.get(t, b, L) for t in (w.k, w.v))
+        o, _, wt, mag, _ = oc.attention(q[b * rows:b * rows + n].double().cpu().numpy(), k, v, np.arange(L - n, L),
+                                        np.arange(L)[:, None].repeat(2, 1), 64 ** -0.5)
+        # scores off by d = 2^-23 (dh + 8) 32 + 2^-20 < 2^-11.8 (sum |q k| scale below 32), p by 4 d; outputs as in
+        # the attention tests: 2 u and 4 d of sum p |v|, one rounding
+        u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+        for got in (full[b * rows:b * rows + n], again[at:at + n]):
+            assert (np.abs(got.double().cpu().numpy() - o) <= u * np.abs(o) + (2 * u + 2.0 ** -9.8) * mag).all()
+        gain = w.get(w.weight, b) - before[b]
+        assert (np.abs(gain[:L] - wt) <= 2.0 ** -9.8 * (wt + 1e-7) + 2.0 ** -22 * (1 + wt)).all() and (gain[L:] == 0).all()
+        at += n
