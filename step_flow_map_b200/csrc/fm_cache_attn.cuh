@@ -556,13 +556,15 @@ __device__ __forceinline__ void weigh_row(const CacheAttnArgs& a, const NewRows&
   for (int x = 0; x < n * a.G; ++x) {
     const int t = s.first + x / a.G, h = g * a.G + x % a.G;
     const int pq = a.q_pos ? __ldg(a.q_pos + t) : s.L - s.n + x / a.G;
-    if (!sees(pq, pk, a.window, a.sinks)) continue;
+    const float lse = a.lse[(size_t)t * a.n_heads + h];
+    // (lse is -inf where all scores are: such a query gives no weight, as its output is 0)
+    if (lse == -INFINITY || !sees(pq, pk, a.window, a.sinks)) continue;
     float d = 0.f;
 #pragma unroll
     for (int k = 0; k < DH / 32; ++k)
       d = fmaf(to_f(((const T*)a.q)[t * a.qs + h * DH + lane + 32 * k]), kv[k], d);
     d = warp_sum(d);
-    sum += exp2f(d * a.scale_log2 - a.lse[(size_t)t * a.n_heads + h] * 1.4426950408889634f);
+    sum += exp2f(d * a.scale_log2 - lse * 1.4426950408889634f);
   }
   if (lane == 0) a.c.weight[at] += sum;
 }

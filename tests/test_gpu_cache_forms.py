@@ -144,3 +144,31 @@ def test_weights_of_accepted_rows_alone(dtype, G):
         gain = w.get(w.weight, b) - before[b]
         assert (np.abs(gain[:L] - wt) <= 2.0 ** -9.8 * (wt + 1e-7) + 2.0 ** -22 * (1 + wt)).all() and (gain[L:] == 0).all()
         at += n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 3, 12, 60])
+def test_a_query_whose_scores_are_all_minus_infinity(dtype, rows):
+    """It gets zeros and gives no weight, as one that sees nothing; the others go on without it."""
+    w = World([200, 90], 2, 64, 16, dtype, seed=rows, weight=True)
+    for b, L in enumerate(w.lens):
+        k = torch.tensor(w.get(w.k, b))
+        k[..., 0] = k[..., 0].abs() + 0.1
+        w.put(w.k, b, k)
+    q = torch.tensor(w.rng.normal(size=(2 * rows, 8, 64))).to(w.k.dtype).cuda()
+    cu, args = cu_of([rows] * 2), dict(max_rows=rows, max_kv=200, lse=True)
+    had = w.weight.clone()
+    want, wl = w.cache.attend(q, cu, w.kv, accumulate=True, **args)
+    all_heads = torch.nan_to_num(w.weight - had)
+    bad = q.clone()
+    bad[rows - 1, 5, 0] = -float("inf")
+    w.weight.copy_(had)
+    got, gl = w.cache.attend(bad, cu, w.kv, accumulate=True, **args)
+    assert (got[rows - 1, 5] == 0).all() and gl[rows - 1, 5] == -float("inf")
+    got[rows - 1, 5], gl[rows - 1, 5] = want[rows - 1, 5], wl[rows - 1, 5]
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+    gain = torch.nan_to_num(w.weight - had, nan=-9.0)
+    # its head's rows lose its one unit of weight, no other row changes (fp32 sums of 200 terms below 61)
+    assert (gain >= 0).all() and (gain <= all_heads + 1e-4).all()
+    lost = (all_heads - gain).sum((0, 2)).cpu()
+    assert abs(lost[1] - 1) < 1e-2 and lost[0].abs() < 1e-4
