@@ -50,8 +50,10 @@ __device__ __forceinline__ NewRows new_rows(const int* cu, const int* kv_len, in
 // rot_dim values turns by position * inv_freq[i]: (a, b) -> (a cos - b sin,
 // b cos + a sin).
 //
-// Bound: HBM (every value read once and written once) for many rows, launch
-// and one chain of dependent loads for few.  A thread holds 16 bytes of one
+// Bound: for many rows the instructions per 16 bytes (12,709 rows, ncu: 0.71
+// issued a cycle and scheduler, DRAM at 55 % of the copy rate; stalls are fixed
+// latencies and the norm's shuffles), then HBM (every value read once and
+// written once); launch and one chain of dependent loads for few.  A thread holds 16 bytes of one
 // head, head_dim * size / 16 neighbouring lanes hold the head, so the norm is
 // a few shuffles and a half-split pair one shuffle.  A CTA takes `tok` rows:
 // its warps find the rows' sequences, pages and angles side by side (one fp64
@@ -60,11 +62,11 @@ __device__ __forceinline__ NewRows new_rows(const int* cu, const int* kv_len, in
 // of its term, in the order the threads read them; a row's angles then sit in
 // registers for all its heads.  Each row is loaded while the row before it is
 // worked on.  (Angles looked up by pair at each use
-// took 108 us for 12,709 rows of 48 heads of width 128 in bf16; this takes 69,
-// 4.5 TB/s.  At 80 registers three CTAs fit an SM; four at 64 took 80 us, two
-// at 96 85.)  tok is 1 while rows are
-// fewer than four per SM and grows to 8, so that the chain at a CTA's start is
-// paid once per 8 rows.
+// took 108 us for 12,709 rows of 48 heads of width 128 in bf16; this takes 72,
+// 4.3 TB/s.  At 80 registers three CTAs fit an SM; four at 64 took 80 us, two
+// at 96 85.)  tok, the rows over four per SM, is 1 while rows are fewer than eight
+// per SM and grows to 8, so that the chain at a CTA's start is paid once per 8
+// rows.
 constexpr int CA_THREADS = 256;
 constexpr int CA_MAX_TOK = 8;     // rows of one CTA
 constexpr int CA_UNROLL = 3;      // 16-byte loads in flight per thread
@@ -180,8 +182,9 @@ __global__ void __launch_bounds__(CA_THREADS, 3) k_cache_append(const AppendArgs
       s_row[j] = row;
       s_page[j] = hit ? cache_page(a.c, seq, row) : -2;   // -2: a row of no sequence
     }
-    // turns = position * f / (2 pi): its whole part drops out in fp64, so the
-    // fraction is good to 1e-10 of a turn at any 32-bit position
+    // turns = position * f / (2 pi), whose whole part drops out: two products and
+    // a constant rounded to fp64, so off by at most 3 2^-53 of the turns, 1e-10 of
+    // a turn up to 300,000 turns and 1.2e-7 at the last 32-bit position (f = 1)
 #pragma unroll
     for (int k = 0; k < PAIRS; ++k) {
       const int i = lane + 32 * k;

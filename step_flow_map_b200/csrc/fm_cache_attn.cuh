@@ -228,9 +228,11 @@ __device__ __forceinline__ void put_join(const CacheAttnArgs& a, const WorkRun& 
 // 64 cache rows, 16 x 16 threads with 4 x 4 scores and 4 x DH / 16 outputs
 // each; scores, probabilities and O stay fp32.  The next block's keys and
 // values come by cp.async while this one is worked on, one CTA barrier a block.
-// Bound: FP32 FMA issue (12 shared-memory wavefronts per 64 FMA instructions of
-// a warp).  513 rows over 1,500, 2 x 12 heads of width 64: 148 us, 26 TFLOP/s
-// (128 threads and loads between the barriers: 257).
+// Bound: shared memory beside the FMAs (12 wavefronts per 64 FMA instructions of
+// a warp; ncu: its data path 68-73 % busy, the FMA pipe 48 %, 0.65 instructions a
+// cycle and scheduler).  513 rows over 1,500, 2 x 12 heads of width 64: 163 us with
+// plan and join, 24 TFLOP/s, a third of the FMA rate (128 threads and loads between
+// the barriers were 1.7 times slower).
 constexpr int CS_THREADS = 256;
 constexpr int CS_KB = 64;
 constexpr int CS_QT = 64;

@@ -8,9 +8,10 @@
 // round trip per 16 keys).  fp32: FMAs, two lanes per key for the scores and
 // DH / 32 columns a lane for the output, four rows at a time, so that few rows
 // cost few instructions.  Measured: one token over 131,071 rows of 8 heads of
-// width 128 in bf16 97 us with the join (107 when both cursors worked out their
-// rows anew for every unit), 64 tokens with weights 167 us (186); 8 tokens over 3,000 rows of 4 heads of
-// width 64 in fp32 24 us with the join (108 in tiles of the prompt kernel).  A unit is 64 cache rows of one (sequence, head); each of
+// width 128 in bf16 98 us with the join (107 when both cursors worked out their
+// rows anew for every unit), 64 tokens with weights 171 us (186); 8 tokens over
+// 3,000 rows of 4 heads of width 64 in fp32 25 us with the join (108 in tiles of
+// the prompt kernel).  A unit is 64 cache rows of one (sequence, head); each of
 // the four warps owns 16 of them and its own three-stage cp.async ring (16
 // rows of a head are one contiguous block of a page), so the loop has no CTA
 // barrier, and the ring runs on across tiles of different sequences.  The

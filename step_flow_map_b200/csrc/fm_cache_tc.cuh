@@ -9,17 +9,21 @@
 // exponentials run under the other's products; two softmax warpgroups work on
 // each, a thread on 64 keys of one packed row (one warpgroup per pair, a thread
 // on all 128 keys: 75 us for 2,777 rows over 4,001, 16 heads of width 64,
-// against 68):
+// against 68 when it was tried):
 //   PAIR  (more than 128 packed rows) the pairs are two tiles of 128 rows that
 //         share every K/V tile;
 //   else  one tile of 128 rows: even blocks go to pair 0, odd ones to pair 1,
 //         merged at the end of the tile.
 // Bound: for prompts the exponentials (16 a clock and SM) and the products, each
 // 43-44 % busy at width 128, where a pair's next S waits for the PV that reads
-// its P; for drafted blocks HBM.  Measured: 8,192 rows, 32 heads of width 128,
-// causal 1.0-1.08 PFLOP/s, under a 2,048 window 317 us (0.76); 2,777 rows over
-// 4,001, width 64, 61 us (0.48); 48 blocks of 17 rows over 2,048..4,096: 135 us
-// with plan and join, 5.6 TB/s inside the kernel.
+// its P; for drafted blocks HBM.  Whole calls, plan and join with them, their
+// inputs not in L2 (the card's power decides the clock, and with it some 3 % of
+// the first three): 8,192 rows, 32 heads of width 128, causal 565 us (0.97
+// PFLOP/s), under a 2,048 window 322 (0.75); 8,192 causal rows of width 64 382
+// (0.72); 2,777 rows over 4,001, 16 heads of width 64, 61 (0.48); 48 blocks of 17
+// rows over 2,048..4,096 136, 5.6 TB/s inside the kernel.  Times beside the
+// choices below compare two builds on one input that stays in L2, called over and
+// over, and are lower.
 //
 // Roles (640 threads): warp 0 TMA, warp 1 MMA, warps 4-19 softmax.
 // O is rescaled by the softmax threads, and only when a row maximum has grown
