@@ -369,12 +369,13 @@ fm_status fm_cache_append(const fm_paged_cache *cache, const fm_append_args *a, 
  *                without it before the verify and score them once more after)
  *   lse          device [T, n_heads] fp32 log-sum-exp of the scores, or NULL
  * With cache->pos q_pos must be given; without it a new row's position is its
- * cache row, whatever q_pos says.  A query that sees nothing, or whose
- * scores are all -inf, gets zeros and lse -inf and gives no weight.  Rows at or past kv_len may hold anything, NaN included, and so may,
- * without cache->pos, rows that no query of the call sees; a non-finite value
- * in any other row can reach all queries of the sequence.  Running maxima, sums
- * and outputs are fp32; bf16 probabilities enter the value product rounded
- * to bf16.  Results do not depend on scheduling.
+ * cache row, whatever q_pos says.  A query that sees nothing, or whose scores
+ * are all -inf, gets zeros and lse -inf and gives no weight.  Rows at or past
+ * kv_len may hold anything, NaN included, and so may, without cache->pos, rows
+ * that no query of the call sees; a non-finite value in any other row can reach
+ * all queries of the sequence.  Running maxima, sums and outputs are fp32; bf16
+ * probabilities enter the value product rounded to bf16.  Results do not depend
+ * on scheduling.
  * ws: device, 256-byte aligned, at least what fm_cache_attention_workspace
  * (some MB; with accumulate and at most 16 new rows x query heads per key/value
  * head 4 bytes more for each of these and each cached row of a head: of B max_kv
