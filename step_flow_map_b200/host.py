@@ -159,6 +159,7 @@ class PagedCache:
             raise ValueError("page_table must be [n_seqs, table_stride]")
         self._check("page_table", t, torch.int32, t.shape)
         self._table = t
+        self._lent = set()         # streams that the cache's tensors are lent to
         self._c.page_table, self._c.table_stride = t.data_ptr(), t.shape[1]
 
     def _check(self, name, t, dtype, shape):
@@ -209,7 +210,10 @@ class PagedCache:
             stream = torch.cuda.ExternalStream(stream, device=self.device)
         elif stream.device != self.device:
             raise ValueError(f"stream of {stream.device}, cache on {self.device}")
-        for t in (self.k, self.v, self.pos, self.weight, self._table, *lent):
+        if stream.cuda_stream not in self._lent:   # (held until they are freed: once per stream is enough)
+            self._lent.add(stream.cuda_stream)
+            lent += (self.k, self.v, self.pos, self.weight, self._table)
+        for t in lent:
             if t is not None:
                 t.record_stream(stream)
         return torch.cuda.stream(stream), stream.cuda_stream
@@ -231,11 +235,11 @@ class PagedCache:
         if inv_freq is not None:
             rot = 2 * inv_freq.shape[0]
             self._check("inv_freq", inv_freq, torch.float64, (rot // 2,))
+        os = n_heads * dh if out is None else self._rows("out", out, T, n_heads)
         ctx, st = self._on(stream, q, k, v, cu_rows, kv_len, q_pos, q_gain, k_gain, inv_freq, out)
         with ctx:
             if out is None:
                 out = q.new_empty(T, n_heads, dh)
-            os = self._rows("out", out, T, n_heads)
             # positional, in the structure's order
             fm_cache_append(self._c, fm_append_args(
                 T, B, n_heads, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
@@ -255,11 +259,11 @@ class PagedCache:
         qs = self._rows("q", q, T, n_heads)
         B = self._seqs(T, cu_rows, kv_len, q_pos)
         self._sizes(max_rows=max_rows, max_kv=max_kv, window=window, sinks=sinks)
+        os = n_heads * dh if out is None else self._rows("out", out, T, n_heads)
         ctx, st = self._on(stream, q, cu_rows, kv_len, q_pos, out)
         with ctx:
             if out is None:
                 out = q.new_empty(T, n_heads, dh)
-            os = self._rows("out", out, T, n_heads)
             got = q.new_empty((T, n_heads), dtype=torch.float32) if lse else None
             a = fm_attention_args(
                 T, B, n_heads, max_rows, max_kv, q.data_ptr(), qs, cu_rows.data_ptr(),
@@ -286,12 +290,12 @@ class PagedCache:
         if B > self._table.shape[0]:
             raise ValueError(f"{B} sequences, {self._table.shape[0]} rows of page_table")
         self._sizes(max_kv=max_kv, budget=budget, sinks=sinks, recent=recent)
+        if new_len is not None:
+            self._check("new_len", new_len, torch.int32, (B,))
         ctx, st = self._on(stream, kv_len, next_pos, new_len)
         with ctx:
             if new_len is None:
                 new_len = kv_len.new_empty(B)
-            else:
-                self._check("new_len", new_len, torch.int32, (B,))
             fm_cache_evict(self._c, kv_len.data_ptr(), next_pos.data_ptr(), B, max_kv, budget, sinks,
                            recent, new_len.data_ptr(), st)
         return new_len

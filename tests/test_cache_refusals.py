@@ -132,3 +132,15 @@ def a_cache_off_the_gpu():
     c = PagedCache(k, k.clone(), torch.zeros(2, 3, dtype=torch.int32), None, torch.zeros(6, 2, 16))
     return (c, torch.zeros(4, 4, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32),
             torch.zeros(2, dtype=torch.int32), torch.zeros(4, 2, 64, dtype=torch.bfloat16))
+
+
+def test_outputs_are_looked_at_before_a_stream_is():
+    """What is wrong with an output is said as for any other tensor, whatever stream is given."""
+    c, q, cu, kv, kr = a_cache_off_the_gpu()
+    for stream in (None, 0):
+        with pytest.raises(ValueError, match="out must"):
+            c.append(q, kr, kr, cu, kv, out=q.float(), stream=stream)
+        with pytest.raises(ValueError, match="out must"):
+            c.attend(q, cu, kv, max_rows=4, max_kv=16, out=q[:3], stream=stream)
+        with pytest.raises(ValueError, match="new_len must"):
+            c.evict(kv, kv, 8, max_kv=16, new_len=kv[:1], stream=stream)

@@ -103,3 +103,19 @@ def test_a_captured_call_on_a_given_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_a_cache_used_on_many_streams_lives_until_all_are_done():
+    """Calls on a first stream, on a second, with another table, and on the first again."""
+    w = World([90, 70], 2, 64, 16, "bf16", pos=True, weight=True)
+    q, cu, pq = torch.randn(6, 4, 64, device="cuda").bfloat16(), cu_of([3, 3]), torch.arange(6, dtype=torch.int32, device="cuda")
+    other = torch.cuda.Stream()
+    for name in ("k", "v", "pos", "weight", "page_table"):
+        def use(t, side):
+            parts = {**{n: getattr(w, n) for n in ("k", "v", "pos", "weight")}, "page_table": w.t, name: t}
+            c = type(w.cache)(**parts)
+            for stream, table in ((other, None), (side, None), (other, w.t.clone()), (side, None)):
+                if table is not None:
+                    c.page_table = table
+                c.attend(q, cu, w.kv, max_rows=3, max_kv=90, q_pos=pq, stream=stream)
+        assert not reused(lambda: (w.t if name == "page_table" else getattr(w, name)).clone(), use), name
